@@ -305,6 +305,79 @@ int dion_plan_timing_read(dion_plan* plan, double* ms_per_phase, int* steps);
  * than as one code. */
 int dion_status(const void* workspace, int count, void* stream, int* per_matrix);
 
+/* ---------------------------------------------------------------------------
+ * Orthogonalization by Newton-Schulz products, and the Muon step.
+ *
+ * For an m x n matrix G, on its smaller side (A is p x p, p = min(m, n)):
+ *   X = G / ||G||_F, then for each iteration k:
+ *   X <- a_k X + (b_k A + c_k A^2) X,   A = X X^T
+ *   O = the last X
+ * which moves every singular value s by s <- a s + b s^3 + c s^5 and keeps
+ * the singular vectors.  coeffs holds steps triples (a, b, c); a triple with
+ * c = 0 is a cubic iteration and takes two products instead of three.  The
+ * usual five quintic iterations take (3.4445, -4.7750, 2.0315) each; the
+ * textbook cubic is (1.5, -0.5, 0).  1 <= steps <= 32.  Coefficients under
+ * which a singular value in [0, 1] can grow past 64 are rejected.
+ *
+ * math: DION_MATH_F32 keeps float32 accuracy (every factor as two float16
+ *   planes, 22 bits, three matrix products per product); DION_MATH_F16 takes
+ *   one float16 product per product (factors rounded to 11 bits between
+ *   products, float32 accumulation): about 1.2e-3 relative error after five
+ *   quintic iterations of an N(0, 1) matrix, below bfloat16's own rounding of
+ *   the result, growing for matrices whose singular values fall off steeply.
+ *
+ * A zero matrix has O = 0.  A matrix with a non-finite entry (or, for the
+ * step, a non-finite momentum) sets DION_STATUS_NONFINITE in its status word
+ * (dion_status) and leaves O, or X and M, as they were.  The conventions at
+ * the top of this header hold, with these differences: G and O have row
+ * pitches ldg, ldo >= n (elements); m, n >= 1 with m n < 2^31 and any order;
+ * a list holds at most DION_MAX_LIST matrices.  The list is read before the
+ * call returns. */
+#define DION_MATH_F16     0x1000
+#define DION_STATUS_NONFINITE 8  /* orthogonalize, muon_step: non-finite input */
+#define DION_MAX_LIST 65536
+
+typedef struct dion_ns_matrix {
+  const void* G;        /* m x n, float32 or bfloat16 per g_dtype, read only */
+  void*       O;        /* m x n, float32 or bfloat16 per o_dtype */
+  int64_t     m, n;
+  int64_t     ldg, ldo; /* row pitches in elements */
+} dion_ns_matrix;
+
+size_t dion_orthogonalize_workspace_size(const dion_ns_matrix* mats, int count, int math);
+int dion_orthogonalize_batched(const dion_ns_matrix* mats, int count,
+                               const float* coeffs, int steps, int math,
+                               int g_dtype, int o_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+int dion_orthogonalize(const void* G, int64_t ldg, void* O, int64_t ldo,
+                       int64_t m, int64_t n, const float* coeffs, int steps, int math,
+                       int g_dtype, int o_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Muon step on dense row-major X, M (float32) and G (float32 or bfloat16):
+ *   M <- mu M + G
+ *   D  = G + mu M (nesterov != 0) or M
+ *   X <- (1 - lr weight_decay) X - lr scale O,   O = orthogonalize(D)
+ * X and M are updated in place.  scale is the caller's per-matrix factor
+ * (for example sqrt(max(1, m / n))). */
+typedef struct dion_muon_matrix {
+  float*      X;        /* m x n, updated in place */
+  const void* G;        /* m x n, read only */
+  float*      M;        /* m x n momentum, updated in place */
+  int64_t     m, n;
+  float       scale;
+} dion_muon_matrix;
+
+size_t dion_muon_workspace_size(const dion_muon_matrix* mats, int count, int math);
+int dion_muon_step_batched(const dion_muon_matrix* mats, int count, float lr, float momentum,
+                           int nesterov, float weight_decay, const float* coeffs, int steps,
+                           int math, int g_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int dion_muon_step(float* X, const void* G, float* M, int64_t m, int64_t n, float scale,
+                   float lr, float momentum, int nesterov, float weight_decay,
+                   const float* coeffs, int steps, int math, int g_dtype,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,8 @@ from typing import List, Optional, Sequence, Tuple
 __all__ = [
     "DionError", "Breakdown", "Plan", "load", "library_path", "workspace_size",
     "workspace_size_batched", "step", "step_batched", "step_noalloc", "status",
-    "check_status", "version", "VARIANTS",
+    "check_status", "version", "VARIANTS", "NS_COEFFS", "orthogonalize", "orthogonalize_batched",
+    "muon_step", "muon_step_batched",
 ]
 
 OK = 0
@@ -36,6 +37,10 @@ SCHED_GROUPED = 0x800   # OR into math: small matrices through the grouped sched
 SHARD_GRAM, SHARD_W = 0, 1
 BUF_W, BUF_P, BUF_U = 1, 2, 3   # dion_plan_buffer: intermediate factors of the last step
 STATUS_ORTH_P, STATUS_ORTH_W, STATUS_COLNORM = 1, 2, 4
+STATUS_NONFINITE = 8   # orthogonalize, muon_step: non-finite input
+MATH_NS = {"f32": 0x0000, "f16": 0x1000}   # orthogonalize, muon_step
+# the quintic Newton-Schulz coefficients in common use
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB: Optional[ctypes.CDLL] = None
@@ -65,6 +70,16 @@ class dion_matrix(ctypes.Structure):
                 ("r", ctypes.c_int64)]
 
 
+class dion_ns_matrix(ctypes.Structure):
+    _fields_ = [("G", ctypes.c_void_p), ("O", ctypes.c_void_p), ("m", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class dion_muon_matrix(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("G", ctypes.c_void_p), ("M", ctypes.c_void_p),
+                ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
 def load() -> ctypes.CDLL:
     """Load libdion.so (built by ``build.py``); raises if it is missing."""
     global _LIB
@@ -79,6 +94,8 @@ def load() -> ctypes.CDLL:
     c_size, c_int, c_i64, c_f, vp = (ctypes.c_size_t, ctypes.c_int, ctypes.c_int64,
                                      ctypes.c_float, ctypes.c_void_p)
     mats_p = ctypes.POINTER(dion_matrix)
+    ns_p, muon_p, f_p = (ctypes.POINTER(dion_ns_matrix), ctypes.POINTER(dion_muon_matrix),
+                         ctypes.POINTER(ctypes.c_float))
     sig = {
         "dion_version": (c_int, []),
         "dion_error_string": (ctypes.c_char_p, [c_int]),
@@ -103,6 +120,16 @@ def load() -> ctypes.CDLL:
                                      ctypes.POINTER(c_size)]),
         "dion_step_noalloc": (c_int, [vp, vp, vp, vp, c_i64, c_i64, c_i64, c_f, c_f, c_int,
                                       c_int, vp, vp]),
+        "dion_orthogonalize_workspace_size": (c_size, [ns_p, c_int, c_int]),
+        "dion_orthogonalize_batched": (c_int, [ns_p, c_int, f_p, c_int, c_int, c_int, c_int, vp,
+                                               c_size, vp]),
+        "dion_orthogonalize": (c_int, [vp, c_i64, vp, c_i64, c_i64, c_i64, f_p, c_int, c_int, c_int,
+                                       c_int, vp, c_size, vp]),
+        "dion_muon_workspace_size": (c_size, [muon_p, c_int, c_int]),
+        "dion_muon_step_batched": (c_int, [muon_p, c_int, c_f, c_f, c_int, c_f, f_p, c_int, c_int,
+                                           c_int, vp, c_size, vp]),
+        "dion_muon_step": (c_int, [vp, vp, vp, c_i64, c_i64, c_f, c_f, c_f, c_int, c_f, f_p, c_int,
+                                   c_int, c_int, vp, c_size, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -396,3 +423,154 @@ def check_status(workspace, count: int, stream=None) -> None:
     if rc == ERR_BREAKDOWN:
         raise Breakdown(rc, load().dion_error_string(rc).decode(), per)
 
+
+
+# --- Newton-Schulz orthogonalization and the Muon step ---------------------
+
+def _ns_coeffs(coeffs, steps: int):
+    """One (a, b, c) for every iteration, or a list of `steps` of them."""
+    rows = list(coeffs)
+    if len(rows) == 3 and all(isinstance(v, (int, float)) for v in rows):
+        rows = [tuple(rows)] * int(steps)
+    if len(rows) != int(steps) or any(len(r) != 3 for r in rows):
+        raise ValueError("coeffs must be (a, b, c) or one (a, b, c) per iteration")
+    flat = [float(v) for r in rows for v in r]
+    return (ctypes.c_float * max(len(flat), 1))(*flat)
+
+
+def _ns_math(math) -> int:
+    if isinstance(math, str):
+        if math not in MATH_NS:
+            raise ValueError(f"math must be one of {list(MATH_NS)}")
+        math = MATH_NS[math]
+    return int(math)
+
+
+def _check_rows(name, t, shape=None, dtypes=None, device=None):
+    """A 2-D GPU tensor whose rows are contiguous; returns its row pitch."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    m, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    pitch = t.stride(0) if m > 1 else n
+    if pitch < n:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return pitch
+
+
+def _scratch(nbytes: int, device, workspace, stream):
+    """The caller's workspace, or a new one; a new one that another stream
+    than the current one will use is marked so for torch's allocator."""
+    ws = _workspace(nbytes, device, workspace)
+    if workspace is None and stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _same_dtype(tensors, name):
+    first = tensors[0].dtype
+    if any(t.dtype != first for t in tensors):
+        raise TypeError(f"every {name} of a grouped call must have the same dtype")
+    return 1 if first == _torch().bfloat16 else 0
+
+
+def orthogonalize_batched(mats: Sequence[Tuple], coeffs=NS_COEFFS, steps: int = 5, math="f32",
+                          workspace=None, stream=None):
+    """Newton-Schulz orthogonalization of a list of (G, O) tensor pairs: O
+    (float32 or bfloat16) receives the orthogonalized G (float32 or
+    bfloat16).  math: "f32" (float32 accuracy) or "f16" (one float16 matrix
+    product per product).  Returns the workspace (for reuse and ``status``)."""
+    torch = _torch()
+    if len(mats) == 0:
+        raise ValueError("empty matrix list")
+    types = (torch.float32, torch.bfloat16)
+    dev = mats[0][0].device
+    arr = (dion_ns_matrix * len(mats))()
+    for i, (G, O) in enumerate(mats):
+        ldg = _check_rows("G", G, None, types, dev)
+        ldo = _check_rows("O", O, G.shape, types, dev)
+        arr[i] = dion_ns_matrix(G.data_ptr(), O.data_ptr(), G.shape[0], G.shape[1], ldg, ldo)
+    gd, od = _same_dtype([g for g, _ in mats], "G"), _same_dtype([o for _, o in mats], "O")
+    mode, cf = _ns_math(math), _ns_coeffs(coeffs, steps)
+    lib = load()
+    nbytes = lib.dion_orthogonalize_workspace_size(arr, len(mats), mode)
+    if nbytes == 0:
+        raise _err(ERR_INVALID_ARG)
+    ws = _scratch(nbytes, dev, workspace, stream)
+    with torch.cuda.device(dev):
+        rc = lib.dion_orthogonalize_batched(arr, len(mats), cf, int(steps), mode, gd, od,
+                                            ws.data_ptr(), nbytes, _stream_handle(stream, dev))
+    if rc != OK:
+        raise _err(rc)
+    return ws
+
+
+def orthogonalize(G, O, coeffs=NS_COEFFS, steps: int = 5, math="f32", workspace=None, stream=None):
+    """``orthogonalize_batched`` of one matrix."""
+    return orthogonalize_batched([(G, O)], coeffs, steps, math, workspace, stream)
+
+
+def _muon_scale(scale, m: int, n: int) -> float:
+    if scale == "none":
+        return 1.0
+    if scale == "spectral":
+        return max(1.0, m / n) ** 0.5
+    if scale == "rms":
+        return 0.2 * max(m, n) ** 0.5
+    if isinstance(scale, str):
+        raise ValueError("scale must be 'none', 'spectral', 'rms' or a number")
+    return float(scale)
+
+
+def muon_step_batched(mats: Sequence[Tuple], lr: float, momentum: float = 0.95,
+                      nesterov: bool = True, weight_decay: float = 0.0, scale="spectral",
+                      coeffs=NS_COEFFS, steps: int = 5, math="f32", workspace=None, stream=None):
+    """Muon step over a list of (X, G, M): M <- momentum M + G, D = G +
+    momentum M (nesterov) or M, X <- (1 - lr weight_decay) X - lr s
+    orthogonalize(D).  X, M float32, updated in place; G float32 or bfloat16.
+    scale: s = 1 ("none"), sqrt(max(1, m / n)) ("spectral"), 0.2
+    sqrt(max(m, n)) ("rms"), or a number.  Returns the workspace."""
+    torch = _torch()
+    if len(mats) == 0:
+        raise ValueError("empty matrix list")
+    dev = mats[0][0].device
+    arr = (dion_muon_matrix * len(mats))()
+    for i, (X, G, M) in enumerate(mats):
+        for name, t, types in (("X", X, (torch.float32,)), ("M", M, (torch.float32,)),
+                               ("G", G, (torch.float32, torch.bfloat16))):
+            if _check_rows(name, t, X.shape, types, dev) != t.shape[1]:
+                raise ValueError(f"{name} must be contiguous (row-major)")
+        m, n = X.shape
+        arr[i] = dion_muon_matrix(X.data_ptr(), G.data_ptr(), M.data_ptr(), m, n,
+                                  _muon_scale(scale, m, n) if m and n else 0.0)
+    gd = _same_dtype([g for _, g, _ in mats], "G")
+    mode, cf = _ns_math(math), _ns_coeffs(coeffs, steps)
+    lib = load()
+    nbytes = lib.dion_muon_workspace_size(arr, len(mats), mode)
+    if nbytes == 0:
+        raise _err(ERR_INVALID_ARG)
+    ws = _scratch(nbytes, dev, workspace, stream)
+    with torch.cuda.device(dev):
+        rc = lib.dion_muon_step_batched(arr, len(mats), float(lr), float(momentum),
+                                        1 if nesterov else 0, float(weight_decay), cf, int(steps),
+                                        mode, gd, ws.data_ptr(), nbytes, _stream_handle(stream, dev))
+    if rc != OK:
+        raise _err(rc)
+    return ws
+
+
+def muon_step(X, G, M, lr: float, momentum: float = 0.95, nesterov: bool = True,
+              weight_decay: float = 0.0, scale="spectral", coeffs=NS_COEFFS, steps: int = 5,
+              math="f32", workspace=None, stream=None):
+    """``muon_step_batched`` of one matrix."""
+    return muon_step_batched([(X, G, M)], lr, momentum, nesterov, weight_decay, scale, coeffs,
+                             steps, math, workspace, stream)

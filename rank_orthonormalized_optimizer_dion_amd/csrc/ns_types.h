@@ -1,0 +1,84 @@
+// Types and launchers of the Newton-Schulz orthogonalization (k_ns.hip,
+// ns_api.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dion {
+
+constexpr int kNsPad = 64;        // rows and columns of every plane are padded to this, with zeros
+constexpr int kNsParts = 512;     // most partial sums of squares per matrix
+constexpr int kNsMaxClasses = 8;
+constexpr int kNsUpload = 24;     // descriptors per table upload (kernel arguments: under 4 KB)
+constexpr int32_t kNsNonFinite = 8;   // status bit: DION_STATUS_NONFINITE
+inline __host__ __device__ int64_t ns_pad(int64_t x) { return (x + kNsPad - 1) / kNsPad * kNsPad; }
+
+// One matrix, seen from its smaller side: the planes hold the p x q matrix
+// (p <= q) that is G or, when G has more rows than columns (tall), its
+// transpose.  Offsets are bytes from the workspace base.
+struct NsDesc {
+  const void* G;    // m x n, pitch ldg
+  void* O;          // orthogonalize: the output (pitch ldo); step: the weights X (float32)
+  float* M;         // step: the momentum; else null
+  int64_t ldg, ldo;
+  int32_t p, q;
+  int32_t tall;
+  int32_t slot;     // index in the caller's list = status word index
+  int32_t parts;    // partial sums of squares
+  int32_t planes;   // 16-bit planes per value: 1 or 2
+  float scale;      // step: the update's factor lr * s
+  int64_t chunk;    // elements of G per partial sum
+  int64_t oX;       // two buffers of PL planes pp x qp (X and the next X), 16-bit
+  int64_t oA, oB;   // PL planes pp x pp each: A = X X^T, B = a I + b A + c A^2
+  int64_t oS;       // parts float64, then the normalization tau (float32)
+};
+
+struct NsClass {
+  int32_t planes;
+  int32_t first, count;   // matrices of this shape in the table
+  int32_t tiles, base;    // work items per matrix, first item
+  int32_t tx, ty;         // tile grid
+};
+
+// What a product's epilogue does.
+enum NsEpi : int32_t {
+  kNsGram = 0,    // A = X X^T
+  kNsGramPoly,    // B = a I + b X X^T (cubic iterations: no A^2)
+  kNsPoly,        // B = a I + b A + c A A^T
+  kNsApply,       // next X = B X
+  kNsOut,         // output = B X
+  kNsStep,        // X <- decay X - scale (B X)
+};
+
+struct NsLaunch {
+  const NsDesc* table;    // device table, or null to use `inl`
+  NsDesc inl;
+  char* ws;
+  int32_t* status;
+  int32_t nclass, total;
+  NsClass cls[kNsMaxClasses];
+  float mu;               // step: momentum; nesterov: D = G + mu M, else D = M
+  int32_t nesterov;
+  float decay;            // step: 1 - lr * weight decay
+  float x0;               // power-of-two scale of the first X's planes
+  float f_acc, f_a, f_i;  // epilogue: f_acc * product + f_a * A + f_i * I
+  int32_t tau;            // f_acc is multiplied by tau^this (first iteration)
+  int32_t src;            // which of the two X buffers is read
+  int32_t gdtype, odtype; // 0 float32, 1 bfloat16
+};
+
+struct NsUpload {
+  NsDesc d[kNsUpload];
+  NsDesc* dst;
+  int32_t count;
+};
+
+hipError_t launch_ns_table(const NsUpload& u, hipStream_t st);
+hipError_t launch_ns_norm(const NsLaunch& L, hipStream_t st);
+hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st);
+// tile: 128 or 256
+hipError_t launch_ns_product(const NsLaunch& L, NsEpi epi, int planes, int tile, hipStream_t st);
+// work items of a symmetric product over an nt x nt tile grid
+int ns_sym_items(int nt);
+
+}  // namespace dion
