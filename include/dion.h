@@ -378,6 +378,59 @@ int dion_muon_step(float* X, const void* G, float* M, int64_t m, int64_t n, floa
                    const float* coeffs, int steps, int math, int g_dtype,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear layer: the products around a weight matrix that the steps above
+ * train.  x is t x k (tokens by inputs), W n x k:
+ *   forward:   z = x W^T + bias;  y = act(z) + residual
+ *   backward:  dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum_t dz
+ * (the residual's gradient is dy itself).  dW is the G that a step reads.
+ *
+ * Every tensor has `dtype` (float32 or bfloat16) except bias and db, which
+ * are float32, and a row pitch in elements (>= its columns); any alignment of
+ * its elements and any t >= 0 (t = 0: dW and db are zero).  bfloat16 products
+ * are exact and summed in float32; act, bias and residual are applied in
+ * float32 and the result is rounded once; backward rounds dz to bfloat16
+ * before the two products when there is an activation and more than 64
+ * tokens.  float32 products are
+ * taken as six bfloat16 products of three-way split operands (24 bits, errors
+ * of float32's order); a non-finite operand makes the outputs it reaches
+ * non-finite, not always with the sign float32 would give.
+ *
+ * Forward reads x, w, bias (or NULL), residual (or NULL; y itself is allowed)
+ * and writes y and, when z is not NULL, z.  Backward reads dy, z (only with
+ * an activation), x (for dw) and w (for dx) and writes those of dx, dw and db
+ * that are not NULL; with accumulate != 0, dw and db are added to.  Outputs
+ * overlap nothing else.  Sums are taken in a fixed order: the same call gives
+ * the same bits.  Size queries return 0 for invalid arguments; errors as for
+ * the calls above. */
+#define DION_ACT_NONE  0
+#define DION_ACT_RELU  1
+#define DION_ACT_RELU2 2   /* max(z, 0)^2 */
+#define DION_ACT_GELU  3   /* z Phi(z), Phi the normal distribution function */
+#define DION_ACT_SILU  4   /* z / (1 + exp(-z)) */
+
+typedef struct dion_linear {
+  int64_t      t, n, k;
+  const void*  x;         int64_t ldx;     /* t x k */
+  const void*  w;         int64_t ldw;     /* n x k */
+  const float* bias;                       /* n */
+  const void*  residual;  int64_t ldr;     /* t x n */
+  void*        y;         int64_t ldy;     /* t x n */
+  void*        z;         int64_t ldz;     /* t x n */
+  const void*  dy;        int64_t lddy;    /* t x n */
+  void*        dx;        int64_t lddx;    /* t x k */
+  void*        dw;        int64_t lddw;    /* n x k */
+  float*       db;                         /* n */
+  int          act;                        /* DION_ACT_* */
+  int          dtype;                      /* DION_DTYPE_* */
+  int          accumulate;
+} dion_linear;
+
+size_t dion_linear_forward_workspace_size(const dion_linear* l);
+int dion_linear_forward(const dion_linear* l, void* workspace, size_t workspace_bytes, void* stream);
+size_t dion_linear_backward_workspace_size(const dion_linear* l);
+int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

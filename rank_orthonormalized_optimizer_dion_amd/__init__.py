@@ -20,7 +20,7 @@ __all__ = [
     "DionError", "Breakdown", "Plan", "load", "library_path", "workspace_size",
     "workspace_size_batched", "step", "step_batched", "step_noalloc", "status",
     "check_status", "version", "VARIANTS", "NS_COEFFS", "orthogonalize", "orthogonalize_batched",
-    "muon_step", "muon_step_batched",
+    "muon_step", "muon_step_batched", "linear_forward", "linear_backward", "ACTS",
 ]
 
 OK = 0
@@ -39,6 +39,7 @@ BUF_W, BUF_P, BUF_U = 1, 2, 3   # dion_plan_buffer: intermediate factors of the 
 STATUS_ORTH_P, STATUS_ORTH_W, STATUS_COLNORM = 1, 2, 4
 STATUS_NONFINITE = 8   # orthogonalize, muon_step: non-finite input
 MATH_NS = {"f32": 0x0000, "f16": 0x1000}   # orthogonalize, muon_step
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}   # linear_forward / _backward
 # the quintic Newton-Schulz coefficients in common use
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
@@ -80,6 +81,21 @@ class dion_muon_matrix(ctypes.Structure):
                 ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
+class dion_linear(ctypes.Structure):
+    _fields_ = [("t", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("db", ctypes.c_void_p),
+                ("act", ctypes.c_int), ("dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
+
+
 def load() -> ctypes.CDLL:
     """Load libdion.so (built by ``build.py``); raises if it is missing."""
     global _LIB
@@ -96,6 +112,7 @@ def load() -> ctypes.CDLL:
     mats_p = ctypes.POINTER(dion_matrix)
     ns_p, muon_p, f_p = (ctypes.POINTER(dion_ns_matrix), ctypes.POINTER(dion_muon_matrix),
                          ctypes.POINTER(ctypes.c_float))
+    lin_p = ctypes.POINTER(dion_linear)
     sig = {
         "dion_version": (c_int, []),
         "dion_error_string": (ctypes.c_char_p, [c_int]),
@@ -130,6 +147,10 @@ def load() -> ctypes.CDLL:
                                            c_int, vp, c_size, vp]),
         "dion_muon_step": (c_int, [vp, vp, vp, c_i64, c_i64, c_f, c_f, c_f, c_int, c_f, f_p, c_int,
                                    c_int, c_int, vp, c_size, vp]),
+        "dion_linear_forward_workspace_size": (c_size, [lin_p]),
+        "dion_linear_forward": (c_int, [lin_p, vp, c_size, vp]),
+        "dion_linear_backward_workspace_size": (c_size, [lin_p]),
+        "dion_linear_backward": (c_int, [lin_p, vp, c_size, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -574,3 +595,104 @@ def muon_step(X, G, M, lr: float, momentum: float = 0.95, nesterov: bool = True,
     """``muon_step_batched`` of one matrix."""
     return muon_step_batched([(X, G, M)], lr, momentum, nesterov, weight_decay, scale, coeffs,
                              steps, math, workspace, stream)
+
+
+# --- linear layer -----------------------------------------------------------
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"act must be one of {list(ACTS)}")
+        act = ACTS[act]
+    return int(act)
+
+
+def _put(s, name, ld, tensor, shape, dtype, device):
+    if tensor is None:
+        return
+    pitch = _check_rows(name, tensor, shape, (dtype,), device)
+    setattr(s, name, tensor.data_ptr())
+    setattr(s, ld, pitch)
+
+
+def _put_vector(s, name, tensor, n, device):
+    if tensor is None:
+        return
+    if not tensor.is_cuda or tensor.device != device or tensor.dtype != _torch().float32:
+        raise TypeError(f"{name} must be a float32 GPU tensor on the same device")
+    if tuple(tensor.shape) != (n,) or not tensor.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    setattr(s, name, tensor.data_ptr())
+
+
+def _linear(name, s, device, workspace, stream):
+    lib = load()
+    size = getattr(lib, f"dion_linear_{name}_workspace_size")(ctypes.byref(s))
+    if size == 0:
+        raise _err(ERR_INVALID_ARG)
+    ws = _scratch(size, device, workspace, stream)
+    with _torch().cuda.device(device):
+        rc = getattr(lib, f"dion_linear_{name}")(ctypes.byref(s), ws.data_ptr(), size,
+                                                 _stream_handle(stream, device))
+    if rc != OK:
+        raise _err(rc)
+    return ws
+
+
+def _linear_dtype(t, name) -> int:
+    torch = _torch()
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return 1 if t.dtype == torch.bfloat16 else 0
+
+
+def linear_forward(x, weight, y, bias=None, act="none", residual=None, preact=None,
+                   workspace=None, stream=None):
+    """y = act(x weight^T + bias) + residual (dion_linear_forward).
+
+    x (t x k), weight (n x k), y, residual, preact (t x n): float32 or
+    bfloat16, one type; bias (n) float32.  act: one of ACTS.  preact receives
+    x weight^T + bias, which the backward of an activation needs.  residual
+    may be y itself.  Returns the workspace."""
+    s = dion_linear(dtype=_linear_dtype(x, "x"), act=_act(act))
+    if weight.dim() != 2:
+        raise ValueError("weight must be 2-D")
+    t, k = x.shape
+    n = weight.shape[0]
+    s.t, s.n, s.k = t, n, k
+    dev = x.device
+    _put(s, "x", "ldx", x, (t, k), x.dtype, dev)
+    _put(s, "w", "ldw", weight, (n, k), x.dtype, dev)
+    _put(s, "y", "ldy", y, (t, n), x.dtype, dev)
+    _put(s, "residual", "ldr", residual, (t, n), x.dtype, dev)
+    _put(s, "z", "ldz", preact, (t, n), x.dtype, dev)
+    _put_vector(s, "bias", bias, n, dev)
+    return _linear("forward", s, dev, workspace, stream)
+
+
+def linear_backward(dy, x=None, weight=None, dx=None, dw=None, db=None, act="none", preact=None,
+                    accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of linear_forward (dion_linear_backward): dz = dy act'(preact),
+    dx = dz weight, dw = dz^T x, db = the sum of dz over tokens, those of the
+    three that are given.  accumulate: add to dw and db.  The residual's
+    gradient is dy.  Returns the workspace."""
+    s = dion_linear(dtype=_linear_dtype(dy, "dy"), act=_act(act), accumulate=int(bool(accumulate)))
+    t, n = dy.shape
+    given = [v.shape[1] for v in (x, weight, dx, dw) if v is not None and v.dim() == 2]
+    k = given[0] if given else 1
+    s.t, s.n, s.k = t, n, k
+    dev = dy.device
+    if s.act and preact is None:
+        raise ValueError("the backward of an activation needs preact")
+    if dx is not None and weight is None or dw is not None and x is None:
+        raise ValueError("dx needs weight, dw needs x")
+    _put(s, "dy", "lddy", dy, (t, n), dy.dtype, dev)
+    _put(s, "z", "ldz", preact if s.act else None, (t, n), dy.dtype, dev)
+    _put(s, "x", "ldx", x, (t, k), dy.dtype, dev)
+    _put(s, "w", "ldw", weight, (n, k), dy.dtype, dev)
+    _put(s, "dx", "lddx", dx, (t, k), dy.dtype, dev)
+    _put(s, "dw", "lddw", dw, (n, k), dy.dtype, dev)
+    _put_vector(s, "db", db, n, dev)
+    return _linear("backward", s, dev, workspace, stream)

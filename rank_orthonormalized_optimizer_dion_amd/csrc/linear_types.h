@@ -1,0 +1,76 @@
+// Types and launchers of the linear layer (k_linear.hip, linear_api.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dion {
+
+// The output side of a product: y = act(acc + bias) + residual with z =
+// acc + bias kept on request, or out (+)= acc.
+struct LinOut {
+  void* y;
+  int64_t ldy;
+  const float* bias;       // or null
+  const void* residual;    // or null
+  int64_t ldr;
+  void* z;                 // or null
+  int64_t ldz;
+  int32_t act;             // DION_ACT_*
+  int32_t dtype;           // of y, residual and z: 0 float32, 1 bfloat16
+  int32_t accumulate;      // out += acc (y only, no bias / act / residual)
+};
+
+// C (M x N) = sum over `nseg` plane pairs of A B^T, reduction length K,
+// split over `splits` slices of `klen`.
+struct LinProduct {
+  const uint16_t* a;
+  const uint16_t* b;
+  int64_t lda, ldb, sa, sb;   // pitches; elements from plane to plane
+  int32_t M, N, K;
+  int32_t nseg;               // 1; 2: A in two planes; 6: both operands in three
+  int32_t splits, klen;
+  int32_t tx, ty;
+  float* part;                // splits > 1: float32 partial products
+  LinOut out;
+};
+
+// Operand layouts of the three products (see mm16.h: K-major or x-major).
+enum LinKind : int32_t {
+  kLinForward = 0,   // x W^T:   both K-major
+  kLinDx,            // dz W:    K-major, x-major
+  kLinDw,            // dz^T x:  both x-major
+};
+
+struct LinPack {
+  const void* src;      // rows x cols, pitch ld; float32 or bfloat16
+  int64_t ld;
+  const void* z;        // pre-activation (dz = src act'(z)), or null
+  int64_t ldz;
+  uint16_t* dst;        // planes, pitch `pitch` >= cols, zero past cols; or null
+  int64_t pitch, plane;
+  float* sums;          // partial column sums, one row per chunk; or null
+  int64_t rows;
+  int32_t cols, chunk;  // rows per workgroup
+  int32_t act, dtype, planes;
+};
+
+struct LinSkinny {
+  const void* x;
+  const void* w;
+  int64_t ldx, ldw;
+  int32_t t, n, k;
+  LinOut out;
+};
+
+constexpr int kSkinnyTokens = 64;   // matrix-core kernel for few tokens
+constexpr int kRowTokens = 8;       // float32 / unaligned kernel for few tokens
+
+hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st);
+hipError_t launch_lin_finish(const LinProduct& p, hipStream_t st);
+hipError_t launch_lin_pack(const LinPack& p, hipStream_t st);
+hipError_t launch_lin_colsum(const float* part, int chunks, int n, float* out, int accumulate,
+                             hipStream_t st);
+hipError_t launch_lin_skinny(const LinSkinny& p, hipStream_t st);
+hipError_t launch_lin_rows(const LinSkinny& p, bool vec, hipStream_t st);
+
+}  // namespace dion

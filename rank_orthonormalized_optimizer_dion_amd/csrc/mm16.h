@@ -48,8 +48,9 @@ struct B16 {
 static __device__ u32x4 g_zero_cell;
 
 // One operand of a tile: `p` the plane (uniform), its pitch, the tile's
-// first x, the number of x and the reduction length K (K-major operands: a
-// multiple of 8).  Cells past K are zero; x past the last re-reads the last
+// first x, the number of x and the reduction length K (K-major operands: the
+// columns from K to the next multiple of 8 exist and are zero).  Cells past
+// K are zero; x past the last re-reads the last
 // x (K-major) or the last 8 x (x-major), which only feeds outputs that are
 // never stored.
 template <int BX, int BK, int NT, bool MC>
