@@ -97,36 +97,42 @@ __device__ __forceinline__ void store8(void* p, int64_t o, int dtype, bool vec, 
   }
 }
 
-// The epilogue of one run of 8 outputs (row, col .. col + 7).
-__device__ __forceinline__ void lin_out(const LinOut& o, int row, int col, int left, const float (&acc)[8]) {
+// What a run of 8 outputs (row, col .. col + 7) adds to the activation or
+// to the product: the residual, or the old output when accumulating.
+struct LinPre {
+  float w[8];
+};
+__device__ __forceinline__ LinPre lin_fetch(const LinOut& o, int row, int col, int left) {
+  LinPre p{};
+  const void* src = o.accumulate ? o.y : o.residual;
+  const int64_t ld = o.accumulate ? o.ldy : o.ldr;
+  if (src) load8(src, row * ld + col, o.dtype, aligned16(src, ld, o.dtype), left, p.w);
+  return p;
+}
+
+// The epilogue of such a run.  ACT: the activation, or -1 for o.act.
+template <int ACT>
+__device__ __forceinline__ void lin_out(const LinOut& o, int row, int col, int left, const float (&acc)[8],
+                                        const LinPre& pre) {
+  const int act = ACT < 0 ? o.act : ACT;
   float v[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = acc[k];
-  const int64_t oy = row * o.ldy + col;
-  const bool vy = aligned16(o.y, o.ldy, o.dtype);
-  if (o.accumulate) {
-    float w[8];
-    load8(o.y, oy, o.dtype, vy, left, w);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += w[k];
-  }
   if (o.bias) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < left) v[k] += o.bias[col + k];
   }
   if (o.z) store8(o.z, row * o.ldz + col, o.dtype, aligned16(o.z, o.ldz, o.dtype), left, v);
-  if (o.act != DION_ACT_NONE) {
+  if (act != DION_ACT_NONE) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], o.act);
+    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], act);
   }
-  if (o.residual) {
-    float w[8];
-    load8(o.residual, row * o.ldr + col, o.dtype, aligned16(o.residual, o.ldr, o.dtype), left, w);
+  if (o.residual || o.accumulate) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += w[k];
+    for (int k = 0; k < 8; ++k) v[k] += pre.w[k];
   }
-  store8(o.y, oy, o.dtype, vy, left, v);
+  store8(o.y, row * o.ldy + col, o.dtype, aligned16(o.y, o.ldy, o.dtype), left, v);
 }
 
 // Plane pairs of a three-way split product, smallest terms first: with x =
@@ -143,10 +149,10 @@ __device__ __forceinline__ void six_pairs(int s, int& a, int& b) {
 }
 
 template <int TILE, LinKind KIND>
-using LinShape = Shape16<B16, TILE, TILE, 64, 2, TILE / 64, 1, KIND == kLinDw, KIND != kLinForward>;
+using LinShape = Shape16<B16, TILE, TILE, TILE / 64, 2, 1, KIND == kLinDw, KIND != kLinForward>;
 
-template <int TILE, LinKind KIND>
-__global__ __launch_bounds__(64 * 2 * TILE / 64) void k_lin_mm(LinProduct p) {
+template <int TILE, LinKind KIND, int ACT>
+__global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
   using S = LinShape<TILE, KIND>;
   __shared__ u32x4 smem[S::LDS_CELLS];
   const int t = xcd_remap(blockIdx.x, gridDim.x);
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(64 * 2 * TILE / 64) void k_lin_mm(LinProduct p) {
   tile_order(t - s * per, p.tx, p.ty, ti, tj);
   const int r0 = ti * TILE, c0 = tj * TILE;
   const int kbeg = s * p.klen, kend = min(p.K, kbeg + p.klen);
-  f32x16 acc[S::FM][S::FN];
+  typename S::Acc acc[S::FM][S::FN];
   typename S::A ta;
   typename S::B tb;
   ta.init(p.lda, r0, p.M);
@@ -172,15 +178,21 @@ __global__ __launch_bounds__(64 * 2 * TILE / 64) void k_lin_mm(LinProduct p) {
   if (p.splits > 1) {
     float* part = p.part + static_cast<int64_t>(s) * p.M * p.N;
     const bool vec = p.N % 4 == 0;
-    tile_rows<S>(acc, smem, [&](int r, int q, const float (&v)[8]) {
+    tile_runs<S, false>(acc, smem, [](int, int) { return NoPre{}; }, [&](int r, int q, const float (&v)[8], NoPre) {
       const int row = r0 + r, col = c0 + q;
       if (row < p.M && col < p.N) store8(part, static_cast<int64_t>(row) * p.N + col, 0, vec, p.N - col, v);
     });
   } else {
-    tile_rows<S>(acc, smem, [&](int r, int q, const float (&v)[8]) {
-      const int row = r0 + r, col = c0 + q;
-      if (row < p.M && col < p.N) lin_out(p.out, row, col, p.N - col, v);
-    });
+    tile_runs<S, false>(
+        acc, smem,
+        [&](int r, int q) {
+          const int row = r0 + r, col = c0 + q;
+          return row < p.M && col < p.N ? lin_fetch(p.out, row, col, p.N - col) : LinPre{};
+        },
+        [&](int r, int q, const float (&v)[8], const LinPre& pre) {
+          const int row = r0 + r, col = c0 + q;
+          if (row < p.M && col < p.N) lin_out<ACT>(p.out, row, col, p.N - col, v, pre);
+        });
   }
 }
 
@@ -199,7 +211,7 @@ __global__ __launch_bounds__(256) void k_lin_finish(LinProduct p) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += w[k];
     }
-    lin_out(p.out, row, col, p.N - col, v);
+    lin_out<-1>(p.out, row, col, p.N - col, v, lin_fetch(p.out, row, col, p.N - col));
   }
 }
 
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(512) void k_lin_skinny(LinSkinny p) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) v[i] += red[s][token >> 4][token & 15][c + i];
     }
-    lin_out(p.out, token, n0 + c, p.n - n0 - c, v);
+    lin_out<-1>(p.out, token, n0 + c, p.n - n0 - c, v, lin_fetch(p.out, token, n0 + c, p.n - n0 - c));
   }
 }
 
@@ -388,19 +400,27 @@ __global__ __launch_bounds__(256) void k_lin_rows(LinSkinny p) {
   for (int i = 0; i < T; ++i)
     if (lane == i && i < p.t) {
       const float v[8] = {acc[i], 0, 0, 0, 0, 0, 0, 0};
-      lin_out(p.out, i, n, 1, v);
+      lin_out<-1>(p.out, i, n, 1, v, lin_fetch(p.out, i, n, 1));
     }
+}
+
+template <int TILE, LinKind KIND, int ACT>
+hipError_t product(const LinProduct& p, hipStream_t st) {
+  k_lin_mm<TILE, KIND, ACT><<<dim3(static_cast<unsigned>(p.tx) * p.ty * p.splits), dim3(2 * TILE), 0, st>>>(p);
+  return hipGetLastError();
 }
 
 template <int TILE>
 hipError_t product(const LinProduct& p, LinKind kind, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.tx) * p.ty * p.splits), block(64 * 2 * TILE / 64);
-  switch (kind) {
-    case kLinForward: k_lin_mm<TILE, kLinForward><<<grid, block, 0, st>>>(p); break;
-    case kLinDx: k_lin_mm<TILE, kLinDx><<<grid, block, 0, st>>>(p); break;
-    case kLinDw: k_lin_mm<TILE, kLinDw><<<grid, block, 0, st>>>(p); break;
+  if (kind == kLinDx) return product<TILE, kLinDx, DION_ACT_NONE>(p, st);
+  if (kind == kLinDw) return product<TILE, kLinDw, DION_ACT_NONE>(p, st);
+  switch (p.out.act) {
+    case DION_ACT_RELU: return product<TILE, kLinForward, DION_ACT_RELU>(p, st);
+    case DION_ACT_RELU2: return product<TILE, kLinForward, DION_ACT_RELU2>(p, st);
+    case DION_ACT_GELU: return product<TILE, kLinForward, DION_ACT_GELU>(p, st);
+    case DION_ACT_SILU: return product<TILE, kLinForward, DION_ACT_SILU>(p, st);
+    default: return product<TILE, kLinForward, DION_ACT_NONE>(p, st);
   }
-  return hipGetLastError();
 }
 
 template <int T>

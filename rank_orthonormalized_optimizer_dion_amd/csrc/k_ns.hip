@@ -110,9 +110,15 @@ __global__ __launch_bounds__(256) void k_ns_norm(NsLaunch L) {
     reinterpret_cast<double*>(L.ws + d.oS)[local] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// Eight values as planes.
+// Where the eight values from (row, col), col a multiple of 8, of a matrix
+// of `pitch` columns sit: their hi parts, and kLoOffset further their lo.
+constexpr int kLoOffset = 16;
 template <int PL>
-__device__ __forceinline__ void store_planes(uint16_t* at, int64_t plane, const float (&v)[8]) {
+__device__ __forceinline__ int64_t plane_at(int64_t row, int col, int64_t pitch) {
+  return PL == 2 ? row * 2 * pitch + (col >> 4) * 32 + (col & 15) : row * pitch + col;
+}
+template <int PL>
+__device__ __forceinline__ void store_planes(uint16_t* at, const float (&v)[8]) {
   uint16_t hi[8], lo[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -121,7 +127,7 @@ __device__ __forceinline__ void store_planes(uint16_t* at, int64_t plane, const 
     if constexpr (PL == 2) lo[k] = to_f16(x - f16_to_f32(hi[k]));
   }
   *reinterpret_cast<u32x4*>(at) = pack8(hi);
-  if constexpr (PL == 2) *reinterpret_cast<u32x4*>(at + plane) = pack8(lo);
+  if constexpr (PL == 2) *reinterpret_cast<u32x4*>(at + kLoOffset) = pack8(lo);
 }
 
 // X = D 2^-e as planes (times the planes' scale), 2^-e the power of two that
@@ -175,7 +181,7 @@ __global__ __launch_bounds__(256) void k_ns_load(NsLaunch L) {
     tile[4 * s + (threadIdx.x >> 6)][threadIdx.x & 63] = v;
   }
   __syncthreads();
-  const int64_t pitch = ns_pad(d.q), plane = ns_pad(d.p) * pitch;
+  const int64_t pitch = ns_pitch(d.q, PL);
   uint16_t* X = reinterpret_cast<uint16_t*>(L.ws + d.oX);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -183,7 +189,7 @@ __global__ __launch_bounds__(256) void k_ns_load(NsLaunch L) {
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = d.tall ? tile[j + k][i] : tile[i][j + k];
-    store_planes<PL>(X + (i0 + i) * pitch + j0 + j, plane, v);
+    store_planes<PL>(X + plane_at<PL>(i0 + i, j0 + j, pitch), v);
   }
 }
 
@@ -203,26 +209,29 @@ __device__ __forceinline__ bool sym_tile(int t, int nt, int& ti, int& tj) {
   return ti <= tj && ti < nt;
 }
 
+// Eight stored values: as loaded, and as numbers.
 template <int PL>
-__device__ __forceinline__ void load_planes(const uint16_t* at, int64_t plane, float (&v)[8]) {
-  const f16x8 hi = __builtin_bit_cast(f16x8, *reinterpret_cast<const u32x4*>(at));
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(hi[k]);
-  if constexpr (PL == 2) {
-    const f16x8 lo = __builtin_bit_cast(f16x8, *reinterpret_cast<const u32x4*>(at + plane));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += static_cast<float>(lo[k]);
+struct NsRun {
+  u32x4 hi, lo;
+  __device__ __forceinline__ void load(const uint16_t* at) {
+    hi = *reinterpret_cast<const u32x4*>(at);
+    if constexpr (PL == 2) lo = *reinterpret_cast<const u32x4*>(at + kLoOffset);
   }
-}
+  __device__ __forceinline__ float value(int k) const {
+    const float h = static_cast<float>(__builtin_bit_cast(f16x8, hi)[k]);
+    if constexpr (PL == 2) return h + static_cast<float>(__builtin_bit_cast(f16x8, lo)[k]);
+    else return h;
+  }
+};
 
 template <int PL, int TILE, bool BMC>
-using NsShape = Shape16<F16, TILE, TILE, PL == 2 ? 32 : 64, 2, TILE / 64, PL, false, BMC>;
+using NsShape = Shape16<F16, TILE, TILE, TILE / 64, 2, PL, false, BMC>;
 
 // One tile of one of the three products.  Products that are symmetric
 // compute the tiles on and above the diagonal and write each one's
 // transpose too.
 template <int PL, int TILE, NsEpi EPI>
-__global__ __launch_bounds__(64 * 2 * TILE / 64) void k_ns_mm(NsLaunch L) {
+__global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
   constexpr bool SYM = EPI == kNsGram || EPI == kNsGramPoly || EPI == kNsPoly;
   using S = NsShape<PL, TILE, !SYM>;
   __shared__ u32x4 smem[S::LDS_CELLS];
@@ -236,31 +245,34 @@ __global__ __launch_bounds__(64 * 2 * TILE / 64) void k_ns_mm(NsLaunch L) {
   } else {
     tile_order(local, c.tx, c.ty, ti, tj);
   }
-  if (L.status[d.slot] & kNsNonFinite) return;
+  if (uniform32(L.status[d.slot]) & kNsNonFinite) return;
 
-  const int pp = static_cast<int>(ns_pad(d.p)), qp = static_cast<int>(ns_pad(d.q));
-  const int64_t planeX = static_cast<int64_t>(pp) * qp, planeA = static_cast<int64_t>(pp) * pp;
-  uint16_t* X = reinterpret_cast<uint16_t*>(L.ws + d.oX) + L.src * PL * planeX;
-  uint16_t* A = reinterpret_cast<uint16_t*>(L.ws + d.oA);
-  uint16_t* B = reinterpret_cast<uint16_t*>(L.ws + d.oB);
+  ti = uniform32(ti);
+  tj = uniform32(tj);
+  const int pp = uniform32(static_cast<int>(ns_pad(d.p))), qp = uniform32(static_cast<int>(ns_pad(d.q)));
+  const int pitchA = uniform32(static_cast<int>(ns_pitch(d.p, PL))), pitchX = uniform32(static_cast<int>(ns_pitch(d.q, PL)));
+  const int64_t planeX = static_cast<int64_t>(pp) * pitchX;
+  uint16_t* X = uniform_at(reinterpret_cast<uint16_t*>(L.ws + d.oX) + L.src * PL * planeX);
+  uint16_t* A = uniform_at(reinterpret_cast<uint16_t*>(L.ws + d.oA));
+  uint16_t* B = uniform_at(reinterpret_cast<uint16_t*>(L.ws + d.oB));
   const int r0 = ti * TILE, c0 = tj * TILE;
 
-  f32x16 acc[S::FM][S::FN];
+  typename S::Acc acc[S::FM][S::FN];
   typename S::A ta;
   typename S::B tb;
   auto one = [](int, int& a, int& b) { a = b = 0; };
   if constexpr (EPI == kNsGram || EPI == kNsGramPoly) {
-    ta.init(qp, r0, pp);
-    tb.init(qp, c0, pp);
-    tile_product<S>(ta, tb, Planes16{X, X, planeX, planeX}, 1, one, 0, qp, smem, acc);
+    ta.init(PL * pitchX, r0, pp);
+    tb.init(PL * pitchX, c0, pp);
+    tile_product<S>(ta, tb, Planes16{X, X, 0, 0}, 1, one, 0, qp, smem, acc);
   } else if constexpr (EPI == kNsPoly) {
-    ta.init(pp, r0, pp);
-    tb.init(pp, c0, pp);
-    tile_product<S>(ta, tb, Planes16{A, A, planeA, planeA}, 1, one, 0, pp, smem, acc);
+    ta.init(PL * pitchA, r0, pp);
+    tb.init(PL * pitchA, c0, pp);
+    tile_product<S>(ta, tb, Planes16{A, A, 0, 0}, 1, one, 0, pp, smem, acc);
   } else {
-    ta.init(pp, r0, pp);
-    tb.init(qp, c0, qp);
-    tile_product<S>(ta, tb, Planes16{B, X, planeA, planeX}, 1, one, 0, pp, smem, acc);
+    ta.init(PL * pitchA, r0, pp);
+    tb.init(PL * pitchX, c0, qp);
+    tile_product<S>(ta, tb, Planes16{B, X, 0, 0}, 1, one, 0, pp, smem, acc);
   }
 
   float f = L.f_acc;
@@ -268,95 +280,108 @@ __global__ __launch_bounds__(64 * 2 * TILE / 64) void k_ns_mm(NsLaunch L) {
     const float tau = *reinterpret_cast<const float*>(L.ws + d.oS + kNsParts * 8);
     f *= L.tau == 2 ? tau * tau : tau;
   }
+  auto none = [](int, int) { return NoPre{}; };
   if constexpr (SYM) {
     uint16_t* dst = EPI == kNsGram ? A : B;
-    auto put = [&](int row, int col, const float (&v)[8]) {
-      if (row >= pp || col >= pp) return;
-      const int64_t o = static_cast<int64_t>(row) * pp + col;
-      float w[8];
-      if constexpr (EPI == kNsPoly) {
-        load_planes<PL>(A + o, planeA, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = fmaf(f, v[k], L.f_a * w[k]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = f * v[k];
-      }
-      if constexpr (EPI != kNsGram) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (row == col + k && row < d.p) w[k] += L.f_i;
-      }
-      store_planes<PL>(dst + o, planeA, w);
+    auto fetch = [&](int row, int col) {
+      NsRun<PL> w{};
+      if (EPI == kNsPoly && row < pp && col < pp) w.load(A + plane_at<PL>(row, col, pitchA));
+      return w;
     };
-    tile_rows<S>(acc, smem, [&](int r, int q, const float (&v)[8]) { put(r0 + r, c0 + q, v); });
-    if (ti != tj) tile_cols<S>(acc, smem, [&](int r, int q, const float (&v)[8]) { put(c0 + r, r0 + q, v); });
+    auto put = [&](int row, int col, const float (&v)[8], const NsRun<PL>& a) {
+      if (row >= pp || col >= pp) return;
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (EPI == kNsPoly) w[k] = fmaf(f, v[k], L.f_a * a.value(k));
+        else w[k] = f * v[k];
+        if constexpr (EPI != kNsGram) {
+          if (row == col + k && row < d.p) w[k] += L.f_i;
+        }
+      }
+      store_planes<PL>(dst + plane_at<PL>(row, col, pitchA), w);
+    };
+    tile_runs<S, false>(acc, smem, [&](int r, int q) { return fetch(r0 + r, c0 + q); },
+                        [&](int r, int q, const float (&v)[8], const NsRun<PL>& a) { put(r0 + r, c0 + q, v, a); });
+    if (ti != tj)
+      tile_runs<S, true>(acc, smem, [&](int r, int q) { return fetch(c0 + r, r0 + q); },
+                         [&](int r, int q, const float (&v)[8], const NsRun<PL>& a) { put(c0 + r, r0 + q, v, a); });
   } else if constexpr (EPI == kNsApply) {
     uint16_t* next = reinterpret_cast<uint16_t*>(L.ws + d.oX) + (1 - L.src) * PL * planeX;
-    tile_rows<S>(acc, smem, [&](int r, int q, const float (&v)[8]) {
+    tile_runs<S, false>(acc, smem, none, [&](int r, int q, const float (&v)[8], NoPre) {
       const int row = r0 + r, col = c0 + q;
       if (row >= pp || col >= qp) return;
       float w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = f * v[k];
-      store_planes<PL>(next + static_cast<int64_t>(row) * qp + col, planeX, w);
+      store_planes<PL>(next + plane_at<PL>(row, col, pitchX), w);
     });
   } else {
     const int rows = d.tall ? d.q : d.p, cols = d.tall ? d.p : d.q;
     const bool vec = (reinterpret_cast<uint64_t>(d.O) & 15) == 0 && d.ldo % (L.odtype ? 8 : 4) == 0;
-    auto put = [&](int row, int col, const float (&v)[8]) {
+    auto fetch = [&](int row, int col) {
+      f32x8 x{};
+      if constexpr (EPI == kNsStep) {
+        const float* at = static_cast<const float*>(d.O) + row * d.ldo + col;
+        if (row < rows && vec && col + 8 <= cols) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(at), b = *reinterpret_cast<const f32x4*>(at + 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[k] = a[k];
+            x[4 + k] = b[k];
+          }
+        } else if (row < rows) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col + k < cols) x[k] = at[k];
+        }
+      }
+      return x;
+    };
+    const float step = d.scale * f;
+    auto put = [&](int row, int col, const float (&v)[8], const f32x8& x) {
       if (row >= rows || col >= cols) return;
       const int64_t o = row * d.ldo + col;
       const int left = cols - col;
-      if constexpr (EPI == kNsStep) {
-        float* x = static_cast<float*>(d.O) + o;
-        const float step = d.scale * f;
-        if (vec && left >= 8) {
-          f32x4 a = *reinterpret_cast<f32x4*>(x), b = *reinterpret_cast<f32x4*>(x + 4);
+      float w[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = fmaf(-step, v[k], L.decay * a[k]);
-            b[k] = fmaf(-step, v[4 + k], L.decay * b[k]);
-          }
-          *reinterpret_cast<f32x4*>(x) = a;
-          *reinterpret_cast<f32x4*>(x + 4) = b;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < left) x[k] = fmaf(-step, v[k], L.decay * x[k]);
-        }
-      } else if (L.odtype) {
-        uint16_t* x = static_cast<uint16_t*>(d.O) + o;
+      for (int k = 0; k < 8; ++k) w[k] = EPI == kNsStep ? fmaf(-step, v[k], L.decay * x[k]) : f * v[k];
+      if (EPI == kNsOut && L.odtype) {
+        uint16_t* at = static_cast<uint16_t*>(d.O) + o;
         uint16_t h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = to_bf16(f * v[k]);
+        for (int k = 0; k < 8; ++k) h[k] = to_bf16(w[k]);
         if (vec && left >= 8) {
-          *reinterpret_cast<u32x4*>(x) = pack8(h);
+          *reinterpret_cast<u32x4*>(at) = pack8(h);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < left) x[k] = h[k];
+            if (k < left) at[k] = h[k];
         }
       } else {
-        float* x = static_cast<float*>(d.O) + o;
+        float* at = static_cast<float*>(d.O) + o;
         if (vec && left >= 8) {
-          *reinterpret_cast<f32x4*>(x) = f32x4{f * v[0], f * v[1], f * v[2], f * v[3]};
-          *reinterpret_cast<f32x4*>(x + 4) = f32x4{f * v[4], f * v[5], f * v[6], f * v[7]};
+          *reinterpret_cast<f32x4*>(at) = f32x4{w[0], w[1], w[2], w[3]};
+          *reinterpret_cast<f32x4*>(at + 4) = f32x4{w[4], w[5], w[6], w[7]};
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < left) x[k] = f * v[k];
+            if (k < left) at[k] = w[k];
         }
       }
     };
-    if (d.tall) tile_cols<S>(acc, smem, [&](int r, int q, const float (&v)[8]) { put(c0 + r, r0 + q, v); });
-    else tile_rows<S>(acc, smem, [&](int r, int q, const float (&v)[8]) { put(r0 + r, c0 + q, v); });
+    if (d.tall)
+      tile_runs<S, true>(acc, smem, [&](int r, int q) { return fetch(c0 + r, r0 + q); },
+                         [&](int r, int q, const float (&v)[8], const f32x8& x) { put(c0 + r, r0 + q, v, x); });
+    else
+      tile_runs<S, false>(acc, smem, [&](int r, int q) { return fetch(r0 + r, c0 + q); },
+                          [&](int r, int q, const float (&v)[8], const f32x8& x) { put(r0 + r, c0 + q, v, x); });
   }
 }
 
 template <int PL, int TILE>
 hipError_t product(const NsLaunch& L, NsEpi epi, hipStream_t st) {
-  const dim3 grid(L.total), block(64 * 2 * TILE / 64);
+  const dim3 grid(L.total), block(2 * TILE);
   switch (epi) {
     case kNsGram: k_ns_mm<PL, TILE, kNsGram><<<grid, block, 0, st>>>(L); break;
     case kNsGramPoly: k_ns_mm<PL, TILE, kNsGramPoly><<<grid, block, 0, st>>>(L); break;

@@ -2,25 +2,30 @@
 // the Newton-Schulz orthogonalization (k_ns.hip) and the linear layer
 // (k_linear.hip).
 //
-// Operands are planes of 16-bit values (float16 or bfloat16) in global
-// memory, row pitch a multiple of 8 elements and 16-byte aligned:
+// Operands are 16-bit values (float16 or bfloat16) in global memory, row
+// pitch a multiple of 8 elements and 16-byte aligned:
 //   K-major   (MC = false): element (x, k) at p[x ld + k]
 //   x-major   (MC = true):  element (x, k) at p[k ld + x]
 // x is the output dimension the operand feeds (a row of C for A, a column
-// of C for B).  A value of more than 16 bits is a sum of PL planes (value =
-// hi + lo); the product is then hi hi + hi lo + lo hi, three matrix
-// instructions per product into the same float32 accumulator.
+// of C for B).  A value of more than 16 bits is a pair hi + lo (PL = 2): rows
+// then hold 16 hi, the 16 lo of the same columns, the next 16 hi, ... (pitch
+// 2 ld), and the product is hi hi + hi lo + lo hi, three matrix instructions
+// per product into the same float32 accumulator.
 //
 // Tiles go from global memory straight to LDS (global_load_lds, 16 bytes per
 // lane), no registers and no conversion.  A wavefront's 64 lanes write 64
 // consecutive 16-byte cells, so a swizzle can only permute which cell of the
-// source each lane fetches:
-//   K-major: cell (x, c), c = k / 8, sits at x (BK / 8) + (c ^ s(x)), so the
-//     ds_read_b128 of an MFMA operand (32 rows x, one c per half wavefront)
-//     touches all bank groups evenly;
-//   x-major: cell (k, c), c = x / 8, sits at k (BX / 8) + (c ^ 4 (k & 3));
-//     ds_read_b64_tr_b16 transposes 4 k by 16 x blocks on the way out.
+// source each lane fetches.  The LDS serves 16 lanes' ds_read_b128 at a time
+// from 64 banks, so 16 consecutive lanes have to cover 16 different cells
+// modulo 16 (with rows of 4 cells and no swizzle half the reads' cycles were
+// bank conflicts):
+//   K-major: cell (x, c) of a row of 4 cells sits at 4 x + (c ^ (x / 4) % 4);
+//   x-major: cell (k, c), c = x / 8, sits at k CPR + (c ^ (4 (k % 4) + 2
+//     (k / 8 % 2))); ds_read_b64_tr_b16 transposes 4 k by 16 x blocks on the
+//     way out.
 #pragma once
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace dion {
@@ -30,16 +35,34 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 template <class T> using lptr = __attribute__((address_space(3))) T*;
 
+// A wavefront-uniform value as a scalar: what came from memory or from the
+// thread index stays in vector registers otherwise, and so do the loop
+// counters and addresses made from it.
+__device__ __forceinline__ int uniform32(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <class T>
+__device__ __forceinline__ T* uniform_at(T* p) {
+  return reinterpret_cast<T*>(uniform64(reinterpret_cast<int64_t>(p)));
+}
+__device__ __forceinline__ int wave16() { return uniform32(static_cast<int>(threadIdx.x >> 6)); }
+
+// Plain products use the 16 x 16 x 32 matrix instruction, pairs of planes the
+// 32 x 32 x 16 one (a stage holds 16 k of a pair).  Both run at the same
+// peak, but the card's power limit sets the clock: on random data an 8192^3
+// float16 product ran at 1120 TFLOP/s with 32 x 32 x 16 and at 1220 with
+// 16 x 16 x 32 (all-zero data: 1740 and 1820).
 struct F16 {
   using Vec = f16x8;
   static __device__ __forceinline__ f32x16 mfma(Vec a, Vec b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
+  static __device__ __forceinline__ f32x4 mfma(Vec a, Vec b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
 };
 struct B16 {
   using Vec = bf16x8;
-  static __device__ __forceinline__ f32x16 mfma(Vec a, Vec b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ f32x4 mfma(Vec a, Vec b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -47,36 +70,38 @@ struct B16 {
 // reduction's end.
 static __device__ u32x4 g_zero_cell;
 
-// One operand of a tile: `p` the plane (uniform), its pitch, the tile's
-// first x, the number of x and the reduction length K (K-major operands: the
-// columns from K to the next multiple of 8 exist and are zero).  Cells past
-// K are zero; x past the last re-reads the last
-// x (K-major) or the last 8 x (x-major), which only feeds outputs that are
-// never stored.
-template <int BX, int BK, int NT, bool MC>
+// One LDS stage holds kStep16 16-bit values of the reduction per x: 32 k, or
+// 16 k as hi and lo.
+constexpr int kStep16 = 32;
+constexpr int kStages16 = 4;
+
+// One operand of a tile: its pitch (2 ld when PL = 2), the tile's first x,
+// the number of x and the reduction length K (K-major operands: the columns
+// from K to the next multiple of 8 exist and are zero).  Cells past K are
+// zero; x past the last re-reads the last x (K-major) or the last 8 x
+// (x-major), which only feeds outputs that are never stored.
+template <int BX, int NT, bool MC, int PL>
 struct Tile16 {
-  static constexpr int CELLS = BX * BK / 8;
-  static constexpr int PER = CELLS / NT;   // loads per thread and tile
-  static_assert(CELLS % NT == 0 && (BK == 32 || BK == 64), "tile does not split over the threads");
-  static constexpr int CPR = MC ? BX / 8 : BK / 8;   // cells per LDS row
+  static constexpr int CELLS = BX * kStep16 / 8;
+  static constexpr int PER = CELLS / NT;   // loads per thread and stage
+  static constexpr int CPR = MC ? PL * BX / 8 : kStep16 / 8;   // cells per LDS row
+  static constexpr int KS = kStep16 / PL;  // k per stage
+  static constexpr int READS = MC ? 2 : 1; // LDS reads per MFMA operand
+  static_assert(CELLS % NT == 0, "tile does not split over the threads");
   uint32_t off[PER];   // byte offset of this lane's source cell at k0 = 0
   int64_t xoff, ld;
 
-  static __device__ __forceinline__ int swz(int row) {
-    if constexpr (MC) return 4 * (row & 3);
-    else if constexpr (BK == 64) return row & 7;
-    else return (row >> 1) & 3;
-  }
+  static __device__ __forceinline__ int swz(int row) { return MC ? 4 * (row & 3) + 2 * ((row >> 3) & 1) : (row >> 2) & 3; }
 
   __device__ __forceinline__ void init(int64_t ld_, int x0, int xn) {
     ld = ld_;
-    xoff = MC ? x0 : x0 * ld_;
+    xoff = MC ? static_cast<int64_t>(PL) * x0 : x0 * ld_;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int c = j * NT + static_cast<int>(threadIdx.x);
       const int row = c / CPR, cell = (c % CPR) ^ swz(row);
       if constexpr (MC) {
-        const int x = min(cell * 8, (xn - x0 - 1) & ~7);
+        const int x = min(cell * 8, (PL * (xn - x0) - 1) & ~7);
         off[j] = static_cast<uint32_t>(row * ld_ * 2 + x * 2);
       } else {
         off[j] = static_cast<uint32_t>(min(row, xn - x0 - 1) * ld_ * 2 + cell * 16);
@@ -84,37 +109,49 @@ struct Tile16 {
     }
   }
 
-  __device__ __forceinline__ void issue(const uint16_t* plane, int k0, int K, u32x4* lds) const {
-    const char* base = reinterpret_cast<const char*>(plane + xoff + (MC ? k0 * ld : static_cast<int64_t>(k0)));
-    const int wave = threadIdx.x >> 6;
-    const bool whole = k0 + BK <= K;
+  // WHOLE: the stage lies inside the reduction.
+  template <bool WHOLE>
+  __device__ __forceinline__ void issue(const uint16_t* p, int k0, int K, u32x4* lds) const {
+    const char* base = reinterpret_cast<const char*>(p + xoff + (MC ? k0 * ld : static_cast<int64_t>(PL) * k0));
+    const int wave = wave16();
+    if constexpr (WHOLE) {
+#if defined(__HIP_DEVICE_COMPILE__)   // the host pass does not know the builtins' types
+      // scalar base, 32-bit lane offsets: no address arithmetic per lane
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_at(base)), 0, 0xffffffffu, 0x00020000);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const char* src = base + off[j];
-      if (!whole) {
+      for (int j = 0; j < PER; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr<void>)(lds + j * NT + wave * 64), 16, off[j], 0, 0, 0);
+#endif
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
         const int c = j * NT + static_cast<int>(threadIdx.x);
         const int row = c / CPR;
-        const int k = k0 + (MC ? row : ((c % CPR) ^ swz(row)) * 8);
-        if (k >= K) src = reinterpret_cast<const char*>(&g_zero_cell);
+        const bool in = MC ? k0 + row < K : PL * k0 + ((c % CPR) ^ swz(row)) * 8 < PL * K;
+        const char* src = in ? base + off[j] : reinterpret_cast<const char*>(&g_zero_cell);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
+                                         (lptr<void>)(lds + j * NT + wave * 64), 16, 0, 0);
       }
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
-                                       (lptr<void>)(lds + j * NT + wave * 64), 16, 0, 0);
     }
   }
 
-  // The MFMA operand of 32 x from x0 (a multiple of 32) and 16 k from 16 q:
-  // lane l holds x = x0 + l % 32, k = 16 q + 8 (l / 32) + 0..7.
+  // PL = 1: the 16 x 16 x 32 operand of the 16 x from x0 (a multiple of 16):
+  // lane l holds x = x0 + l % 16, k = 8 (l / 16) + 0..7.
+  // PL = 2: the 32 x 32 x 16 operand of the 32 x from x0 (a multiple of 32):
+  // lane l holds x = x0 + l % 32 and the hi (f = 0) or lo (f = 1) of k =
+  // 8 (l / 32) + 0..7.
   template <class V>
-  static __device__ __forceinline__ V frag(const u32x4* lds, int x0, int q) {
+  static __device__ __forceinline__ V frag(const u32x4* lds, int x0, int f) {
     const int lane = threadIdx.x & 63;
     if constexpr (!MC) {
-      const int row = x0 + (lane & 31), c = 2 * q + (lane >> 5);
+      const int row = x0 + (PL == 1 ? lane & 15 : lane & 31), c = PL == 1 ? lane >> 4 : 2 * f + (lane >> 5);
       return __builtin_bit_cast(V, lds[row * CPR + (c ^ swz(row))]);
     } else {
       const int i = lane & 15;
-      const int k = 16 * q + 8 * (lane >> 5) + (i >> 2);
-      const int cell = (x0 >> 3) + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-      const char* at = reinterpret_cast<const char*>(lds + k * CPR + (cell ^ swz(i >> 2))) + 8 * (i & 1);
+      const int k = 8 * (PL == 1 ? lane >> 4 : lane >> 5) + (i >> 2);
+      const int block = (x0 >> 4) + (PL == 1 ? 0 : (lane >> 4) & 1);   // 16 x
+      const int cell = (PL == 1 ? 2 * block : 4 * block + 2 * f) + ((i & 3) >> 1);
+      const char* at = reinterpret_cast<const char*>(lds + k * CPR + (cell ^ swz(k))) + 8 * (i & 1);
       struct { s16x4 a, b; } v;
       v.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr<s16x4>)(const_cast<char*>(at)));
       v.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr<s16x4>)(const_cast<char*>(at + 4 * CPR * 16)));
@@ -123,172 +160,299 @@ struct Tile16 {
   }
 };
 
-// Shape of one tile product: BM x BN outputs, BK reduction steps per LDS
-// stage, WM x WN wavefronts, PL planes per operand.
-template <class E_, int BM_, int BN_, int BK_, int WM_, int WN_, int PL_, bool AMC_, bool BMC_>
+// Shape of one tile product: BM x BN outputs, WM x WN wavefronts.
+template <class E_, int BM_, int BN_, int WM_, int WN_, int PL_, bool AMC_, bool BMC_>
 struct Shape16 {
   using E = E_;
-  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, PL = PL_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PL = PL_;
   static constexpr int NT = 64 * WM * WN;
-  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-  using A = Tile16<BM, BK, NT, AMC_>;
-  using B = Tile16<BN, BK, NT, BMC_>;
-  static constexpr int STAGE = PL * (A::CELLS + B::CELLS);   // 16-byte cells
-  // epilogue staging: one 32 x TN block of floats per wavefront, rows padded
-  // by 4, or its transpose (TN = 64: two 32 x 32 blocks, 32 rows of 64)
+  static constexpr int TM = BM / WM, TN = BN / WN;
+  static constexpr int F = PL == 1 ? 16 : 32;            // side of a matrix instruction's output
+  static constexpr int FM = TM / F, FN = TN / F;
+  using Acc = typename std::conditional<PL == 1, f32x4, f32x16>::type;
+  using A = Tile16<BM, NT, AMC_, PL>;
+  using B = Tile16<BN, NT, BMC_, PL>;
+  static constexpr int STAGE = A::CELLS + B::CELLS;   // 16-byte cells
+  static constexpr int PER = A::PER + B::PER;         // loads per thread and stage
+  // epilogue staging: one 64 x 64 block of floats per wavefront, rows padded by 4
   static constexpr int EPITCH = 68;
-  static constexpr int ECELLS = WM * WN * 32 * EPITCH / 4;
-  static constexpr int LDS_CELLS = 2 * STAGE > ECELLS ? 2 * STAGE : ECELLS;
-  static_assert(TN == 64 && TM % 64 == 0, "the epilogue stages 64-wide blocks");
+  static constexpr int ECELLS = WM * WN * 64 * EPITCH / 4;
+  static constexpr int LDS_CELLS = kStages16 * STAGE > ECELLS ? kStages16 * STAGE : ECELLS;
+  static_assert(TN % 64 == 0 && TM % 64 == 0, "the epilogue stages 64-wide blocks");
 };
 
-// A sum over reduction segments: segment s multiplies plane as[s] of A by
-// plane bs[s] of B over the same K.  One segment for plain products, six for
-// three-way split operands.
+// A sum over reduction segments: segment s multiplies plane `a` of A by
+// plane `b` of B over the same K (three-way split operands: planes apart by
+// sa, sb elements).
 struct Planes16 {
   const uint16_t* a;
   const uint16_t* b;
-  int64_t sa, sb;   // elements from one plane to the next
+  int64_t sa, sb;
 };
 
 template <class S>
-__device__ __forceinline__ void tile_mma(const u32x4* st, f32x16 (&acc)[S::FM][S::FN]) {
-  using V = typename S::E::Vec;
-  const int wave = threadIdx.x >> 6;
-  const int xm = (wave / S::WN) * S::TM, xn = (wave % S::WN) * S::TN;
-  const u32x4* a = st;
-  const u32x4* b = st + S::PL * S::A::CELLS;
+using Vec16 = typename S::E::Vec;
+
+// The operands of wavefront rows m0 .. m0 + M - 1 of A, and of all its
+// columns of B.
+template <class S, int M>
+__device__ __forceinline__ void load_a(Vec16<S> (&a)[M], const u32x4* st, int m0, int f) {
+  const int xm = (wave16() / S::WN) * S::TM;
 #pragma unroll
-  for (int q = 0; q < S::BK / 16; ++q) {
-    V fa[S::PL][S::FM], fb[S::PL][S::FN];
+  for (int m = 0; m < M; ++m) a[m] = S::A::template frag<Vec16<S>>(st, xm + S::F * (m0 + m), f);
+}
+template <class S>
+__device__ __forceinline__ void load_b(Vec16<S> (&b)[S::FN], const u32x4* st, int f) {
+  const int xn = (wave16() % S::WN) * S::TN;
 #pragma unroll
-    for (int p = 0; p < S::PL; ++p) {
+  for (int n = 0; n < S::FN; ++n) b[n] = S::B::template frag<Vec16<S>>(st + S::A::CELLS, xn + S::F * n, f);
+}
+template <class S, int M>
+__device__ __forceinline__ void mma16(const Vec16<S> (&a)[M], const Vec16<S> (&b)[S::FN], int m0,
+                                      typename S::Acc (&acc)[S::FM][S::FN]) {
 #pragma unroll
-      for (int n = 0; n < S::FN; ++n) fb[p][n] = S::B::template frag<V>(b + p * S::B::CELLS, xn + 32 * n, q);
+  for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int m = 0; m < S::FM; ++m) fa[p][m] = S::A::template frag<V>(a + p * S::A::CELLS, xm + 32 * m, q);
-    }
-#pragma unroll
-    for (int m = 0; m < S::FM; ++m)
-#pragma unroll
-      for (int n = 0; n < S::FN; ++n) {
-        if constexpr (S::PL == 2) {
-          acc[m][n] = S::E::mfma(fa[1][m], fb[0][n], acc[m][n]);
-          acc[m][n] = S::E::mfma(fa[0][m], fb[1][n], acc[m][n]);
-        }
-        acc[m][n] = S::E::mfma(fa[0][m], fb[0][n], acc[m][n]);
-      }
+    for (int n = 0; n < S::FN; ++n) acc[m0 + m][n] = S::E::mfma(a[m], b[n], acc[m0 + m][n]);
+}
+
+// Waits until at most N of this wavefront's loads are outstanding, then for
+// the other wavefronts: what they loaded before is in LDS for everybody.
+template <int N>
+__device__ __forceinline__ void arrive16() {
+  static_assert(N < 64, "vmcnt holds 6 bits");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The instruction mix of one cluster of M matrix instructions: R LDS reads
+// spread over the first half of them, then G direct loads over the rest, so
+// that they issue in the matrix pipe's shadow instead of before it.  (The
+// loads write LDS, so the compiler keeps them behind the reads.)
+template <int M, int R, int G, int I = 0>
+__device__ __forceinline__ void interleave16() {
+  if constexpr (I < M) {
+    constexpr int H = M / 2;
+    constexpr int r = I < H ? (I + 1) * R / H - I * R / H : 0;
+    constexpr int g = I >= H ? (I + 1 - H) * G / (M - H) - (I - H) * G / (M - H) : 0;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    if constexpr (g > 0) __builtin_amdgcn_sched_group_barrier(0x010, g, 0);
+    interleave16<M, R, G, I + 1>();
   }
 }
 
-// acc = sum over nseg segments and k in [kbeg, kend) (kbeg a multiple of
-// BK).  Two LDS stages: the loads of step t + 1 are in flight during the
-// matrix instructions of step t, and one barrier per step both publishes
-// the stage just loaded and frees the one just read.
+// acc = sum over nseg segments and k in [kbeg, kend).
+//
+// Four LDS stages.  A step t runs two clusters of matrix instructions.
+// During the first it reads the rest of stage t's operands; then it meets the
+// other wavefronts (stage t + 1 has arrived; everybody is done with stage
+// t - 1); during the second it reads the first operands of stage t + 1 and
+// starts the loads of stage t + 3.  So loads have two steps to arrive, and a
+// wavefront always has a cluster whose operands are in registers when it
+// reaches the barrier.  Two wavefronts per SIMD (256 x 256 tiles) or two
+// workgroups per CU (128 x 128) fill each other's gaps.
+// kend - kbeg is a multiple of a stage's k.
+template <class S, class Seg>
+__device__ __forceinline__ void tile_loop(const typename S::A& ta, const typename S::B& tb,
+                                          const Planes16& pl, int total, Seg seg, int kbeg,
+                                          int kend, u32x4* smem, typename S::Acc (&acc)[S::FM][S::FN]) {
+  int is = 0, ik = kbeg;   // segment and reduction offset of the next issue
+  auto stage = [&](int t) { return smem + (t & (kStages16 - 1)) * S::STAGE; };
+  auto issue = [&](int t) {
+    int ia, ib;
+    seg(is, ia, ib);
+    u32x4* st = stage(t);
+    ta.template issue<true>(pl.a + ia * pl.sa, ik, kend, st);
+    tb.template issue<true>(pl.b + ib * pl.sb, ik, kend, st + S::A::CELLS);
+    ik += S::A::KS;
+    const bool wrap = ik >= kend;
+    ik = wrap ? kbeg : ik;
+    is += wrap;
+  };
+  issue(0);
+  if (total > 1) issue(1);
+  if (total > 2) issue(2);
+  if (total > 2) arrive16<2 * S::PER>();
+  else if (total > 1) arrive16<S::PER>();
+  else arrive16<0>();
+  auto arrive = [&](int t) {   // stage t + 1 is there
+    if (t + 2 < total) arrive16<S::PER>();
+    else arrive16<0>();
+  };
+  constexpr int RA = S::A::READS, RB = S::B::READS;
+  int t = 0;
+  if constexpr (S::PL == 1) {
+    // clusters: the upper and the lower half of the wavefront's rows
+    constexpr int H = S::FM / 2;
+    Vec16<S> a0[H], a1[H], b0[S::FN], b1[S::FN];
+    auto step = [&](int t, Vec16<S> (&b)[S::FN], Vec16<S> (&next)[S::FN]) {
+      load_a<S>(a1, stage(t), H, 0);
+      mma16<S>(a0, b, 0, acc);
+      interleave16<H * S::FN, H * RA, 0>();
+      arrive16<S::PER>();
+      load_a<S>(a0, stage(t + 1), 0, 0);
+      load_b<S>(next, stage(t + 1), 0);
+      issue(t + 3);
+      mma16<S>(a1, b, H, acc);
+      interleave16<H * S::FN, H * RA + S::FN * RB, S::PER>();
+    };
+    load_a<S>(a0, smem, 0, 0);
+    load_b<S>(b0, smem, 0);
+    for (; t < total - 4; t += 2) {
+      step(t, b0, b1);
+      step(t + 1, b1, b0);
+    }
+    for (; t < total; ++t) {
+      load_a<S>(a1, stage(t), H, 0);
+      mma16<S>(a0, b0, 0, acc);
+      mma16<S>(a1, b0, H, acc);
+      if (t + 1 < total) {
+        arrive(t);
+        if (t + 3 < total) issue(t + 3);
+        load_a<S>(a0, stage(t + 1), 0, 0);
+        load_b<S>(b0, stage(t + 1), 0);
+      }
+    }
+  } else {
+    // clusters: hi hi and hi lo, then lo hi
+    constexpr int MM = S::FM * S::FN, RR = S::FM * RA + S::FN * RB;
+    Vec16<S> ah[S::FM], bh[S::FN], al[S::FM], bl[S::FN];
+    load_a<S>(ah, smem, 0, 0);
+    load_b<S>(bh, smem, 0);
+    for (; t < total - 3; ++t) {
+      load_b<S>(bl, stage(t), 1);
+      load_a<S>(al, stage(t), 0, 1);
+      mma16<S>(ah, bh, 0, acc);
+      mma16<S>(ah, bl, 0, acc);
+      interleave16<2 * MM, RR, 0>();
+      arrive16<S::PER>();
+      Vec16<S> next[S::FN];
+      load_a<S>(ah, stage(t + 1), 0, 0);
+      load_b<S>(next, stage(t + 1), 0);
+      issue(t + 3);
+      mma16<S>(al, bh, 0, acc);
+      interleave16<MM, RR, S::PER>();
+#pragma unroll
+      for (int n = 0; n < S::FN; ++n) bh[n] = next[n];
+    }
+    for (; t < total; ++t) {
+      load_b<S>(bl, stage(t), 1);
+      load_a<S>(al, stage(t), 0, 1);
+      mma16<S>(ah, bh, 0, acc);
+      mma16<S>(ah, bl, 0, acc);
+      mma16<S>(al, bh, 0, acc);
+      if (t + 1 < total) {
+        arrive(t);
+        load_a<S>(ah, stage(t + 1), 0, 0);
+        load_b<S>(bh, stage(t + 1), 0);
+      }
+    }
+  }
+}
+
 template <class S, class Seg>
 __device__ __forceinline__ void tile_product(const typename S::A& ta, const typename S::B& tb,
                                              const Planes16& pl, int nseg, Seg seg, int kbeg,
                                              int kend, u32x4* smem,
-                                             f32x16 (&acc)[S::FM][S::FN]) {
+                                             typename S::Acc (&acc)[S::FM][S::FN]) {
 #pragma unroll
   for (int m = 0; m < S::FM; ++m)
 #pragma unroll
-    for (int n = 0; n < S::FN; ++n)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.0f;
-  const int nk = (kend - kbeg + S::BK - 1) / S::BK;
-  const int total = nk * nseg;
-  if (total <= 0) return;
-  int is = 0, ik = kbeg;   // segment and reduction offset of the next issue
-  auto issue = [&](u32x4* st) {
+    for (int n = 0; n < S::FN; ++n) acc[m][n] = typename S::Acc{};
+  const int len = kend - kbeg;
+  if (len <= 0) return;
+  const int kfull = kend - len % S::A::KS;
+  const int total = (kfull - kbeg) / S::A::KS * nseg;
+  if (total > 0) {
+    tile_loop<S>(ta, tb, pl, total, seg, kbeg, kfull, smem, acc);
+    __syncthreads();   // the stages become the tail's, or the epilogue's staging area
+  }
+  // the ragged end of the reduction: one stage per segment
+  for (int s = 0; kfull < kend && s < nseg; ++s) {
     int ia, ib;
-    seg(is, ia, ib);
-    const uint16_t* a = pl.a + ia * pl.sa;
-    const uint16_t* b = pl.b + ib * pl.sb;
-#pragma unroll
-    for (int p = 0; p < S::PL; ++p) {
-      ta.issue(a + p * pl.sa, ik, kend, st + p * S::A::CELLS);
-      tb.issue(b + p * pl.sb, ik, kend, st + S::PL * S::A::CELLS + p * S::B::CELLS);
+    seg(s, ia, ib);
+    ta.template issue<false>(pl.a + ia * pl.sa, kfull, kend, smem);
+    tb.template issue<false>(pl.b + ib * pl.sb, kfull, kend, smem + S::A::CELLS);
+    arrive16<0>();
+    Vec16<S> a[S::FM], b[S::FN];
+    load_a<S>(a, smem, 0, 0);
+    load_b<S>(b, smem, 0);
+    mma16<S>(a, b, 0, acc);
+    if constexpr (S::PL == 2) {
+      Vec16<S> al[S::FM], bl[S::FN];
+      load_a<S>(al, smem, 0, 1);
+      load_b<S>(bl, smem, 1);
+      mma16<S>(a, bl, 0, acc);
+      mma16<S>(al, b, 0, acc);
     }
-    ik += S::BK;
-    if (ik >= kend) {
-      ik = kbeg;
-      ++is;
-    }
-  };
-  issue(smem);
-  for (int t = 0; t < total; ++t) {
     __syncthreads();
-    if (t + 1 < total) issue(smem + ((t + 1) & 1) * S::STAGE);
-    tile_mma<S>(smem + (t & 1) * S::STAGE, acc);
   }
-  __syncthreads();   // the stages become the epilogue's staging area
 }
 
-// Hands the tile's values to out(row, col, v) in runs of 8 along a row,
+// Hands the tile's values to out(row, col, v, pre) in runs of 8 along a row,
 // row and col relative to the tile, through LDS (each wavefront its own
-// 32 x 64 floats): the accumulators hold 4 consecutive rows of one column
-// per lane, and every consumer wants whole row segments.
-template <class S, class Out>
-__device__ __forceinline__ void tile_rows(const f32x16 (&acc)[S::FM][S::FN], u32x4* smem, Out out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// 64 x 64 floats): the accumulators hold 4 consecutive rows of one column
+// per lane, and every consumer wants whole row segments.  pre = fetch(row,
+// col) is what the run needs from global memory; a batch of four runs is
+// fetched before the first of them is written, because the compiler cannot
+// move a load over a store to memory it may alias.
+// TRANS: the tile's transpose instead: out(col, row, v, pre) with v the 8
+// rows row .. row + 7 of one column.
+template <class S, bool TRANS, class Fetch, class Out>
+__device__ __forceinline__ void tile_runs(const typename S::Acc (&acc)[S::FM][S::FN], u32x4* smem, Fetch fetch, Out out) {
+  const int lane = threadIdx.x & 63, wave = wave16();
   const int xm = (wave / S::WN) * S::TM, xn = (wave % S::WN) * S::TN;
-  float* buf = reinterpret_cast<float*>(smem) + wave * 32 * S::EPITCH;
+  float* buf = reinterpret_cast<float*>(smem) + wave * 64 * S::EPITCH;
+  constexpr int B = 64 / S::F;   // blocks per side of the staged piece
+  // lane l holds column l % F of a block and, from row 4 (l / F), 4 rows
+  // (16 x 16) or 4 groups of 4 rows, 8 rows apart (32 x 32)
+  const int col = lane & (S::F - 1), row = 4 * (lane / S::F);
 #pragma unroll
-  for (int m = 0; m < S::FM; ++m) {
+  for (int m = 0; m < S::FM; m += B)
 #pragma unroll
-    for (int n = 0; n < S::FN; ++n)
+    for (int n = 0; n < S::FN; n += B) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        buf[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * S::EPITCH + 32 * n + (lane & 31)] = acc[m][n][v];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+      for (int mm = 0; mm < B; ++mm)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 3), c = 8 * (lane & 7);
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(buf + r * S::EPITCH + c);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(buf + r * S::EPITCH + c + 4);
-      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      out(xm + 32 * m + r, xn + c, v);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  }
-}
-
-// The same for the transposed tile: out(col, row, v) with v the 8 rows
-// row .. row + 7 of one column.
-template <class S, class Out>
-__device__ __forceinline__ void tile_cols(const f32x16 (&acc)[S::FM][S::FN], u32x4* smem, Out out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int xm = (wave / S::WN) * S::TM, xn = (wave % S::WN) * S::TN;
-  float* buf = reinterpret_cast<float*>(smem) + wave * 32 * S::EPITCH;
+        for (int nn = 0; nn < B; ++nn) {
+          const typename S::Acc& a = acc[m + mm][n + nn];
 #pragma unroll
-  for (int n = 0; n < S::FN; ++n)
+          for (int q = 0; q < (S::PL == 1 ? 1 : 4); ++q) {
+            const int r = S::F * mm + 8 * q + row, c = S::F * nn + col;
+            if constexpr (TRANS) {
+              *reinterpret_cast<f32x4*>(buf + c * S::EPITCH + r) =
+                  f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            } else {
 #pragma unroll
-    for (int m = 0; m < S::FM; m += 2) {
-#pragma unroll
-      for (int mm = 0; mm < 2; ++mm)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& a = acc[m + mm][n];
-          *reinterpret_cast<f32x4*>(buf + (lane & 31) * S::EPITCH + 32 * mm + 8 * q + 4 * (lane >> 5)) =
-              f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+              for (int v = 0; v < 4; ++v) buf[(r + v) * S::EPITCH + c] = a[4 * q + v];
+            }
+          }
         }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
+      const int r0 = (TRANS ? xn + S::F * n : xm + S::F * m) + (lane >> 3);
+      const int c0 = (TRANS ? xm + S::F * m : xn + S::F * n) + 8 * (lane & 7);
+      const float* at = buf + (lane >> 3) * S::EPITCH + 8 * (lane & 7);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        decltype(fetch(0, 0)) pre[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 3), c = 8 * (lane & 7);
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(buf + r * S::EPITCH + c);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(buf + r * S::EPITCH + c + 4);
-        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        out(xn + 32 * n + r, xm + 32 * m + c, v);
+        for (int i = 0; i < 4; ++i) pre[i] = fetch(r0 + 32 * h + 8 * i, c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* p = at + (32 * h + 8 * i) * S::EPITCH;
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+          const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          out(r0 + 32 * h + 8 * i, c0, v, pre[i]);
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
 }
+struct NoPre {};
 
 // Round to nearest even.
 __device__ __forceinline__ uint16_t to_f16(float x) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)); }

@@ -107,10 +107,10 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
     d.chunk = std::max<int64_t>(8192, ns_cdiv(ns_cdiv(total, kNsParts), 1024) * 1024);
     d.parts = static_cast<int32_t>(ns_cdiv(total, d.chunk));
     d.planes = d.p <= kNsSmallSide ? 2 : planes;
-    const int64_t pp = ns_pad(d.p), qp = ns_pad(d.q);
-    d.oX = take(static_cast<size_t>(2 * d.planes * pp * qp) * 2);
-    d.oA = take(static_cast<size_t>(d.planes * pp * pp) * 2);
-    d.oB = take(static_cast<size_t>(d.planes * pp * pp) * 2);
+    const size_t row = 2 * d.planes * ns_pad(d.p);
+    d.oX = take(2 * row * ns_pitch(d.q, d.planes));
+    d.oA = take(row * ns_pitch(d.p, d.planes));
+    d.oB = take(row * ns_pitch(d.p, d.planes));
     d.oS = take(kNsParts * 8 + 16);
     p.table[g] = d;
     if (g == 0 || mats[order[g]].m != mats[order[g - 1]].m || mats[order[g]].n != mats[order[g - 1]].n) {

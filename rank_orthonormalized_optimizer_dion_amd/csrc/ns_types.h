@@ -12,6 +12,14 @@ constexpr int kNsMaxClasses = 8;
 constexpr int kNsUpload = 24;     // descriptors per table upload (kernel arguments: under 4 KB)
 constexpr int32_t kNsNonFinite = 8;   // status bit: DION_STATUS_NONFINITE
 inline __host__ __device__ int64_t ns_pad(int64_t x) { return (x + kNsPad - 1) / kNsPad * kNsPad; }
+// Row pitch (values) of a plane of x columns: an odd number of 256-byte
+// units, the granularity at which addresses go round the L2 channels.  A
+// tile reads a piece of the same columns of many rows at once; at a pitch of
+// a power of two all of them come from one channel.
+inline __host__ __device__ int64_t ns_pitch(int64_t x, int planes) {
+  const int64_t unit = 128 / planes;
+  return ((ns_pad(x) + unit - 1) / unit | 1) * unit;
+}
 
 // One matrix, seen from its smaller side: the planes hold the p x q matrix
 // (p <= q) that is G or, when G has more rows than columns (tall), its
@@ -28,8 +36,10 @@ struct NsDesc {
   int32_t planes;   // 16-bit planes per value: 1 or 2
   float scale;      // step: the update's factor lr * s
   int64_t chunk;    // elements of G per partial sum
-  int64_t oX;       // two buffers of PL planes pp x qp (X and the next X), 16-bit
-  int64_t oA, oB;   // PL planes pp x pp each: A = X X^T, B = a I + b A + c A^2
+  // pp = ns_pad(p), qp = ns_pad(q), 16-bit, `planes` per value (mm16.h),
+  // pitches ns_pitch:
+  int64_t oX;       // two buffers of pp x qp (X and the next X)
+  int64_t oA, oB;   // pp x pp each: A = X X^T, B = a I + b A + c A^2
   int64_t oS;       // parts float64, then the normalization tau (float32)
 };
 
