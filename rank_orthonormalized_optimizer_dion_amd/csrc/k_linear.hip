@@ -155,13 +155,13 @@ template <int TILE, LinKind KIND, int ACT>
 __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
   using S = LinShape<TILE, KIND>;
   __shared__ u32x4 smem[S::LDS_CELLS];
-  const int t = xcd_remap(blockIdx.x, gridDim.x);
-  const int per = p.tx * p.ty;
-  const int s = t / per;
+  const Work16 work{p.full, p.slices, p.part, p.count};
+  const Item16 it = item16(work, xcd_remap(blockIdx.x, gridDim.x));
   int ti, tj;
-  tile_order(t - s * per, p.tx, p.ty, ti, tj);
+  tile_order(it.tile, p.tx, p.ty, ti, tj);
   const int r0 = ti * TILE, c0 = tj * TILE;
-  const int kbeg = s * p.klen, kend = min(p.K, kbeg + p.klen);
+  int kbeg, kend;
+  slice16<S>(it, p.K, kbeg, kend);
   typename S::Acc acc[S::FM][S::FN];
   typename S::A ta;
   typename S::B tb;
@@ -175,44 +175,21 @@ __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
                     if (nseg == 6) six_pairs(i, a, b);
                   },
                   kbeg, kend, smem, acc);
-  if (p.splits > 1) {
-    float* part = p.part + static_cast<int64_t>(s) * p.M * p.N;
-    const bool vec = p.N % 4 == 0;
-    tile_runs<S, false>(acc, smem, [](int, int) { return NoPre{}; }, [&](int r, int q, const float (&v)[8], NoPre) {
-      const int row = r0 + r, col = c0 + q;
-      if (row < p.M && col < p.N) store8(part, static_cast<int64_t>(row) * p.N + col, 0, vec, p.N - col, v);
-    });
-  } else {
-    tile_runs<S, false>(
-        acc, smem,
-        [&](int r, int q) {
-          const int row = r0 + r, col = c0 + q;
-          return row < p.M && col < p.N ? lin_fetch(p.out, row, col, p.N - col) : LinPre{};
-        },
-        [&](int r, int q, const float (&v)[8], const LinPre& pre) {
-          const int row = r0 + r, col = c0 + q;
-          if (row < p.M && col < p.N) lin_out<ACT>(p.out, row, col, p.N - col, v, pre);
-        });
-  }
+  if (!join16<S>(work, it, smem, acc)) return;
+  tile_runs<S, false>(
+      acc, smem,
+      [&](int r, int q) {
+        const int row = r0 + r, col = c0 + q;
+        return row < p.M && col < p.N ? lin_fetch(p.out, row, col, p.N - col) : LinPre{};
+      },
+      [&](int r, int q, const float (&v)[8], const LinPre& pre) {
+        const int row = r0 + r, col = c0 + q;
+        if (row < p.M && col < p.N) lin_out<ACT>(p.out, row, col, p.N - col, v, pre);
+      });
 }
 
-// The sum of the slices' partial products and the epilogue.
-__global__ __launch_bounds__(256) void k_lin_finish(LinProduct p) {
-  const int groups = (p.N + 7) / 8;
-  const int64_t total = static_cast<int64_t>(groups) * p.M;
-  const bool vec = p.N % 4 == 0;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int row = static_cast<int>(i / groups), col = 8 * static_cast<int>(i - static_cast<int64_t>(row) * groups);
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < p.splits; ++s) {
-      float w[8];
-      load8(p.part + static_cast<int64_t>(s) * p.M * p.N, static_cast<int64_t>(row) * p.N + col, 0, vec, p.N - col, w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += w[k];
-    }
-    lin_out<-1>(p.out, row, col, p.N - col, v, lin_fetch(p.out, row, col, p.N - col));
-  }
+__global__ __launch_bounds__(256) void k_lin_zero(uint32_t* count, int n) {
+  for (int i = threadIdx.x; i < n; i += 256) count[i] = 0;
 }
 
 // dz = src act'(z) (or src itself) as planes with the columns past `cols`
@@ -406,7 +383,7 @@ __global__ __launch_bounds__(256) void k_lin_rows(LinSkinny p) {
 
 template <int TILE, LinKind KIND, int ACT>
 hipError_t product(const LinProduct& p, hipStream_t st) {
-  k_lin_mm<TILE, KIND, ACT><<<dim3(static_cast<unsigned>(p.tx) * p.ty * p.splits), dim3(2 * TILE), 0, st>>>(p);
+  k_lin_mm<TILE, KIND, ACT><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -442,10 +419,8 @@ hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipSt
   return tile == 256 ? product<256>(p, kind, st) : product<128>(p, kind, st);
 }
 
-hipError_t launch_lin_finish(const LinProduct& p, hipStream_t st) {
-  const int64_t groups = static_cast<int64_t>((p.N + 7) / 8) * p.M;
-  const int64_t blocks = (groups + 255) / 256;
-  k_lin_finish<<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st>>>(p);
+hipError_t launch_lin_zero(uint32_t* count, int n, hipStream_t st) {
+  k_lin_zero<<<dim3(1), dim3(256), 0, st>>>(count, n);
   return hipGetLastError();
 }
 

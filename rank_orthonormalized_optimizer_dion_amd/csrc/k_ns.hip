@@ -69,6 +69,8 @@ __global__ __launch_bounds__(256) void k_ns_norm(NsLaunch L) {
   int local;
   ns_locate(L, blockIdx.x, d, c, local);
   if (local == 0 && threadIdx.x == 0) L.status[d.slot] = 0;
+  if (blockIdx.x == 0 && L.count)
+    for (int i = threadIdx.x; i < kNsCounts; i += 256) L.count[i] = 0;
   const int n = d.tall ? d.p : d.q;   // columns as the caller stores them
   const int64_t total = static_cast<int64_t>(d.p) * d.q;
   const int64_t beg = local * d.chunk;
@@ -193,20 +195,26 @@ __global__ __launch_bounds__(256) void k_ns_load(NsLaunch L) {
   }
 }
 
-// Upper-triangle tiles of an nt x nt grid in groups of 4 tile rows: group g
-// holds columns 4 g .. nt - 1, four rows each, walked down the rows first,
-// so that concurrent tiles share row and column panels.  The few items of a
-// group that fall below the diagonal return at once.
+// Upper-triangle tiles of an nt x nt grid in groups of 4 tile rows, each
+// walked down its rows first, so that concurrent tiles share row and column
+// panels: a group starting at row f has the triangle of its first 4 columns,
+// then whole columns of 4.
 constexpr int kSymRows = 4;
-__device__ __forceinline__ bool sym_tile(int t, int nt, int& ti, int& tj) {
+__device__ __forceinline__ void sym_tile(int t, int nt, int& ti, int& tj) {
+  constexpr int TRI = kSymRows * (kSymRows + 1) / 2;
   int first = 0;
-  while (t >= kSymRows * (nt - first)) {
-    t -= kSymRows * (nt - first);
+  while (nt - first > kSymRows && t >= TRI + kSymRows * (nt - first - kSymRows)) {
+    t -= TRI + kSymRows * (nt - first - kSymRows);
     first += kSymRows;
   }
-  ti = first + t % kSymRows;
-  tj = first + t / kSymRows;
-  return ti <= tj && ti < nt;
+  if (t < TRI) {
+    const int j = (t >= 1) + (t >= 3) + (t >= 6);
+    ti = first + t - j * (j + 1) / 2;
+    tj = first + j;
+  } else {
+    ti = first + (t - TRI) % kSymRows;
+    tj = first + kSymRows + (t - TRI) / kSymRows;
+  }
 }
 
 // Eight stored values: as loaded, and as numbers.
@@ -238,10 +246,12 @@ __global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
   NsDesc d;
   NsClass c;
   int local;
-  ns_locate(L, xcd_remap(blockIdx.x, gridDim.x), d, c, local);
+  const Work16 work{L.full, L.slices, L.part, L.count};
+  const Item16 it = item16(work, xcd_remap(blockIdx.x, gridDim.x));
+  ns_locate(L, it.tile, d, c, local);
   int ti, tj;
   if constexpr (SYM) {
-    if (!sym_tile(local, c.tx, ti, tj)) return;
+    sym_tile(local, c.tx, ti, tj);
   } else {
     tile_order(local, c.tx, c.ty, ti, tj);
   }
@@ -261,19 +271,23 @@ __global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
   typename S::A ta;
   typename S::B tb;
   auto one = [](int, int& a, int& b) { a = b = 0; };
+  int kbeg, kend;
+  slice16<S>(it, EPI == kNsGram || EPI == kNsGramPoly ? qp : pp, kbeg, kend);
   if constexpr (EPI == kNsGram || EPI == kNsGramPoly) {
     ta.init(PL * pitchX, r0, pp);
     tb.init(PL * pitchX, c0, pp);
-    tile_product<S>(ta, tb, Planes16{X, X, 0, 0}, 1, one, 0, qp, smem, acc);
+    tile_product<S>(ta, tb, Planes16{X, X, 0, 0}, 1, one, kbeg, kend, smem, acc);
   } else if constexpr (EPI == kNsPoly) {
     ta.init(PL * pitchA, r0, pp);
     tb.init(PL * pitchA, c0, pp);
-    tile_product<S>(ta, tb, Planes16{A, A, 0, 0}, 1, one, 0, pp, smem, acc);
+    tile_product<S>(ta, tb, Planes16{A, A, 0, 0}, 1, one, kbeg, kend, smem, acc);
   } else {
     ta.init(PL * pitchA, r0, pp);
     tb.init(PL * pitchX, c0, qp);
-    tile_product<S>(ta, tb, Planes16{B, X, 0, 0}, 1, one, 0, pp, smem, acc);
+    tile_product<S>(ta, tb, Planes16{B, X, 0, 0}, 1, one, kbeg, kend, smem, acc);
   }
+
+  if (!join16<S>(work, it, smem, acc)) return;
 
   float f = L.f_acc;
   if (L.tau) {
@@ -380,8 +394,8 @@ __global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
 }
 
 template <int PL, int TILE>
-hipError_t product(const NsLaunch& L, NsEpi epi, hipStream_t st) {
-  const dim3 grid(L.total), block(2 * TILE);
+hipError_t product(const NsLaunch& L, int items, NsEpi epi, hipStream_t st) {
+  const dim3 grid(items), block(2 * TILE);
   switch (epi) {
     case kNsGram: k_ns_mm<PL, TILE, kNsGram><<<grid, block, 0, st>>>(L); break;
     case kNsGramPoly: k_ns_mm<PL, TILE, kNsGramPoly><<<grid, block, 0, st>>>(L); break;
@@ -394,12 +408,6 @@ hipError_t product(const NsLaunch& L, NsEpi epi, hipStream_t st) {
 }
 
 }  // namespace
-
-int ns_sym_items(int nt) {
-  int items = 0;
-  for (int first = 0; first < nt; first += kSymRows) items += kSymRows * (nt - first);
-  return items;
-}
 
 hipError_t launch_ns_table(const NsUpload& u, hipStream_t st) {
   k_ns_table<<<dim3(1), dim3(256), 0, st>>>(u);
@@ -425,9 +433,9 @@ hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_ns_product(const NsLaunch& L, NsEpi epi, int planes, int tile, hipStream_t st) {
-  if (planes == 2) return tile == 256 ? product<2, 256>(L, epi, st) : product<2, 128>(L, epi, st);
-  return tile == 256 ? product<1, 256>(L, epi, st) : product<1, 128>(L, epi, st);
+hipError_t launch_ns_product(const NsLaunch& L, int items, NsEpi epi, int planes, int tile, hipStream_t st) {
+  if (planes == 2) return tile == 256 ? product<2, 256>(L, items, epi, st) : product<2, 128>(L, items, epi, st);
+  return tile == 256 ? product<1, 256>(L, items, epi, st) : product<1, 128>(L, items, epi, st);
 }
 
 }  // namespace dion

@@ -7,6 +7,7 @@
 
 #include "dion.h"
 #include "linear_types.h"
+#include "work16.h"
 
 #define DION_API extern "C" __attribute__((visibility("default")))
 
@@ -24,8 +25,7 @@ constexpr int64_t kLinDirectPitch = int64_t{1} << 22;
 // tokens it takes two planes (hi + lo) instead: its roundings average over
 // too few terms there, and the products' time is the weights' traffic.
 constexpr int kLinFewTokens = 64;
-constexpr int kLinFill = 256;      // workgroups that fill the chip
-constexpr int kLinMinSlice = 512;  // shortest reduction slice of a split
+constexpr int64_t kLinBigTiles = 256;   // 256 x 256 tiles in a product of at least this many
 
 struct Span {
   const void* p;
@@ -195,22 +195,21 @@ hipError_t lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, in
   p.K = static_cast<int32_t>(K);
   p.nseg = nseg;
   p.out = out;
-  // 256 x 256 tiles where they fill the chip, else 128 x 128, split over
-  // the reduction while workgroups are missing and slices stay long
-  const int64_t big = lin_cdiv(M, 256) * lin_cdiv(N, 256);
-  const int tile = big >= kLinFill ? 256 : 128;
+  // 256 x 256 tiles where they fill the chip
+  const int tile = lin_cdiv(M, 256) * lin_cdiv(N, 256) >= kLinBigTiles ? 256 : 128;
   p.tx = static_cast<int32_t>(lin_cdiv(M, tile));
   p.ty = static_cast<int32_t>(lin_cdiv(N, tile));
-  const int64_t tiles = static_cast<int64_t>(p.tx) * p.ty;
-  int64_t splits = 1;
-  if (tiles < kLinFill)
-    splits = std::max<int64_t>(1, std::min(lin_cdiv(2 * kLinFill, tiles), K * p.nseg / kLinMinSlice));
-  p.klen = static_cast<int32_t>(lin_cdiv(lin_cdiv(std::max<int64_t>(K, 1), splits), 64) * 64);
-  p.splits = static_cast<int32_t>(std::max<int64_t>(1, lin_cdiv(K, p.klen)));
-  if (p.splits > 1) p.part = r.ws.take<float>(static_cast<size_t>(p.splits) * M * N);
+  const Cut16 c = cut_tiles(static_cast<int64_t>(p.tx) * p.ty, tile, lin_cdiv(K, 32) * nseg);
+  p.items = static_cast<int32_t>(c.items());
+  p.full = static_cast<int32_t>(c.full);
+  p.slices = static_cast<int32_t>(c.slices);
+  if (c.cut) {
+    p.part = r.ws.take<float>(cut_bytes(c, tile) / 4);
+    p.count = r.ws.take<uint32_t>(c.cut);
+  }
   if (!r.go) return hipSuccess;
-  LIN_TRY(launch_lin_product(p, kind, tile, r.st));
-  return p.splits > 1 ? launch_lin_finish(p, r.st) : hipSuccess;
+  if (c.cut) LIN_TRY(launch_lin_zero(p.count, static_cast<int>(c.cut), r.st));
+  return launch_lin_product(p, kind, tile, r.st);
 }
 
 hipError_t lin_forward(Run& r, const LinCall& c) {

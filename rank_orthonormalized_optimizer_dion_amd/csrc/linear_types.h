@@ -20,17 +20,18 @@ struct LinOut {
   int32_t accumulate;      // out += acc (y only, no bias / act / residual)
 };
 
-// C (M x N) = sum over `nseg` plane pairs of A B^T, reduction length K,
-// split over `splits` slices of `klen`.
+// C (M x N) = sum over `nseg` plane pairs of A B^T, reduction length K.
 struct LinProduct {
   const uint16_t* a;
   const uint16_t* b;
   int64_t lda, ldb, sa, sb;   // pitches; elements from plane to plane
   int32_t M, N, K;
   int32_t nseg;               // 1; 2: A in two planes; 6: both operands in three
-  int32_t splits, klen;
   int32_t tx, ty;
-  float* part;                // splits > 1: float32 partial products
+  int32_t items;              // workgroups
+  int32_t full, slices;       // mm16.h, Work16
+  float* part;
+  uint32_t* count;
   LinOut out;
 };
 
@@ -66,7 +67,7 @@ constexpr int kSkinnyTokens = 64;   // matrix-core kernel for few tokens
 constexpr int kRowTokens = 8;       // float32 / unaligned kernel for few tokens
 
 hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st);
-hipError_t launch_lin_finish(const LinProduct& p, hipStream_t st);
+hipError_t launch_lin_zero(uint32_t* count, int n, hipStream_t st);
 hipError_t launch_lin_pack(const LinPack& p, hipStream_t st);
 hipError_t launch_lin_colsum(const float* part, int chunks, int n, float* out, int accumulate,
                              hipStream_t st);

@@ -391,6 +391,92 @@ __device__ __forceinline__ void tile_product(const typename S::A& ta, const type
   }
 }
 
+// How a launch's tiles share the chip.  Tiles 0 .. full - 1 are one
+// workgroup's each.  The rest, less than a round of the chip's workgroup
+// slots, would leave most of it idle for a whole tile's time: each of them is
+// cut along the reduction into `slices` workgroups.
+struct Work16 {
+  int32_t full, slices;
+  float* part;       // a tile of float32 per slice of the cut tiles
+  uint32_t* count;   // one per cut tile, zero between launches
+};
+struct Item16 {
+  int tile, slice, slices, cut;   // cut: index among the cut tiles
+};
+__device__ __forceinline__ Item16 item16(const Work16& w, int t) {
+  if (t < w.full) return {t, 0, 1, 0};
+  const int u = t - w.full;
+  return {w.full + u / w.slices, u % w.slices, w.slices, u / w.slices};
+}
+
+// The slice of [0, K) that an item works on, in whole stages.
+template <class S>
+__device__ __forceinline__ void slice16(const Item16& it, int K, int& kbeg, int& kend) {
+  const int stages = (K + S::A::KS - 1) / S::A::KS, per = (stages + it.slices - 1) / it.slices * S::A::KS;
+  kbeg = min(K, it.slice * per);
+  kend = min(K, kbeg + per);
+}
+
+// Joins the slices of a cut tile: each leaves its sums in global memory; the
+// workgroup that comes last (no one waits) adds all of them up in the order
+// of the slices, whoever it is, so the result does not depend on the order of
+// arrival.  Returns whether this workgroup goes on to the epilogue.
+//
+// The slices run on different XCDs, whose L2s do not see each other's lines.
+// The sums are written and read with device-scope accesses, which go past
+// them, so that waiting for one's own stores is enough: a device-scope fence
+// would write back and invalidate the XCD's whole L2, once per wavefront (the
+// 2048 x 2048 float32 case took 2.4 ms with it, 0.98 ms uncut).
+template <class S>
+__device__ __forceinline__ bool join16(const Work16& w, const Item16& it, u32x4* smem,
+                                       typename S::Acc (&acc)[S::FM][S::FN]) {
+  if (it.slices == 1) return true;
+  constexpr int Q = sizeof(typename S::Acc) / 8, CELLS = S::BM * S::BN / 2;
+  uint64_t* tile = reinterpret_cast<uint64_t*>(w.part) + static_cast<int64_t>(it.cut) * it.slices * CELLS + threadIdx.x;
+  uint64_t* mine = tile + it.slice * CELLS;
+#pragma unroll
+  for (int m = 0; m < S::FM; ++m)
+#pragma unroll
+    for (int n = 0; n < S::FN; ++n)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        struct { float a, b; } v = {acc[m][n][2 * q], acc[m][n][2 * q + 1]};
+        __hip_atomic_store(mine + ((m * S::FN + n) * Q + q) * S::NT, __builtin_bit_cast(uint64_t, v),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's sums have arrived
+  __syncthreads();
+  uint32_t* flag = reinterpret_cast<uint32_t*>(smem);
+  if (threadIdx.x == 0)
+    *flag = __hip_atomic_fetch_add(w.count + it.cut, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last = *flag == static_cast<uint32_t>(it.slices - 1);
+  __syncthreads();   // the flag's cell becomes staging area
+  if (!last) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(w.count + it.cut, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int m = 0; m < S::FM; ++m)
+#pragma unroll
+    for (int n = 0; n < S::FN; ++n) acc[m][n] = typename S::Acc{};
+  for (int s = 0; s < it.slices; ++s) {
+    const uint64_t* src = tile + s * CELLS;
+#pragma unroll
+    for (int m = 0; m < S::FM; ++m)
+#pragma unroll
+      for (int n = 0; n < S::FN; ++n)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          struct F2 { float a, b; };
+          const F2 v = __builtin_bit_cast(F2, __hip_atomic_load(src + ((m * S::FN + n) * Q + q) * S::NT,
+                                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+          acc[m][n][2 * q] += v.a;
+          acc[m][n][2 * q + 1] += v.b;
+        }
+  }
+  return true;
+}
+
 // Hands the tile's values to out(row, col, v, pre) in runs of 8 along a row,
 // row and col relative to the tile, through LDS (each wavefront its own
 // 64 x 64 floats): the accumulators hold 4 consecutive rows of one column

@@ -9,6 +9,7 @@
 
 #include "dion.h"
 #include "ns_types.h"
+#include "work16.h"
 
 #define DION_API extern "C" __attribute__((visibility("default")))
 
@@ -22,6 +23,8 @@ namespace {
 // came out 4.6e-3 off with one plane, where large ones are 1.2e-3 off), and
 // launches, not products, are its cost.
 constexpr int kNsSmallSide = 128;
+constexpr int64_t kNsBigTiles = 256;   // 256 x 256 tiles in a launch of at least this many
+static_assert(kNsCounts >= kTileSlots128 && kNsCounts >= kTileSlots256, "arrival counters");
 constexpr size_t kNsAlign = 256;
 size_t ns_align(size_t x) { return (x + kNsAlign - 1) / kNsAlign * kNsAlign; }
 int64_t ns_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -38,7 +41,7 @@ struct NsMatrix {
 struct NsPlan {
   std::vector<NsDesc> table;      // grouped by shape
   std::vector<NsClass> shapes;    // first, count of each shape
-  size_t status_off = 0, table_off = 0, bytes = 0;
+  size_t status_off = 0, table_off = 0, count_off = 0, part_off = 0, bytes = 0;
 };
 
 bool ns_math(int math, int& planes) {
@@ -71,6 +74,78 @@ int ns_validate(const NsMatrix& a, int gdtype, int odtype, bool step) {
   return DION_OK;
 }
 
+// One grouped launch per kNsMaxClasses shapes; planes: 0 for all shapes, else
+// those with that many planes.
+template <class Fill, class Go>
+hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, int planes, Fill fill, Go go) {
+  NsLaunch L = base;
+  L.nclass = 0;
+  L.total = 0;
+  for (const NsClass& s : p.shapes) {
+    if (planes != 0 && s.planes != planes) continue;
+    NsClass c = s;
+    fill(p.table[s.first], c);
+    c.base = L.total;
+    L.cls[L.nclass++] = c;
+    L.total += c.count * c.tiles;
+    if (L.nclass == kNsMaxClasses) {
+      const hipError_t e = go(L);
+      if (e != hipSuccess) return e;
+      L.nclass = 0;
+      L.total = 0;
+    }
+  }
+  return L.nclass > 0 ? go(L) : hipSuccess;
+}
+
+#define NS_TRY(expr)              \
+  do {                            \
+    const hipError_t e_ = (expr); \
+    if (e_ != hipSuccess) return e_; \
+  } while (0)
+
+// The launches of one product over all matrices of a plan with `planes`
+// planes: go(L, items, tile) with L's classes and work split filled in.
+// 256 x 256 tiles where they fill the chip, else 128 x 128; the largest
+// matrices come first, so that the cut tiles of the last round are the
+// smallest matrices'.
+template <class Go>
+hipError_t ns_launches(const NsPlan& p, const NsLaunch& base, NsEpi epi, int planes, Go go) {
+  const bool sym = epi == kNsGram || epi == kNsGramPoly || epi == kNsPoly;
+  auto shape = [&](int tile) {
+    return [=](const NsDesc& d, NsClass& c) {
+      c.tx = static_cast<int32_t>(ns_cdiv(ns_pad(d.p), tile));
+      c.ty = sym ? c.tx : static_cast<int32_t>(ns_cdiv(ns_pad(d.q), tile));
+      c.tiles = sym ? ns_sym_tiles(c.tx) : c.tx * c.ty;
+    };
+  };
+  int64_t big = 0;
+  for (const NsClass& s : p.shapes) {
+    if (s.planes != planes) continue;
+    NsClass c = s;
+    shape(256)(p.table[s.first], c);
+    big += static_cast<int64_t>(c.tiles) * c.count;
+  }
+  if (big == 0) return hipSuccess;
+  const int tile = big >= kNsBigTiles ? 256 : 128;
+  return ns_grouped(p, base, planes, shape(tile), [&](NsLaunch L) {
+    const NsDesc& d = p.table[L.cls[L.nclass - 1].first];
+    const int64_t k = ns_pad(epi == kNsGram || epi == kNsGramPoly ? d.q : d.p);
+    const Cut16 c = cut_tiles(L.total, tile, k * planes / 32);
+    L.full = static_cast<int32_t>(c.full);
+    L.slices = static_cast<int32_t>(c.slices);
+    return go(L, c, tile);
+  });
+}
+
+hipError_t ns_product(const NsPlan& p, const NsLaunch& base, NsEpi epi, hipStream_t st) {
+  for (int planes = 1; planes <= 2; ++planes)
+    NS_TRY(ns_launches(p, base, epi, planes, [&](const NsLaunch& L, const Cut16& c, int tile) {
+      return launch_ns_product(L, static_cast<int>(c.items()), epi, planes, tile, st);
+    }));
+  return hipSuccess;
+}
+
 // Descriptors grouped by shape, and the workspace: status words, table,
 // then each matrix's planes.
 void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
@@ -78,7 +153,8 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
   std::vector<int> order(count);
   for (int i = 0; i < count; ++i) order[i] = i;
   std::stable_sort(order.begin(), order.end(), [&](int x, int y) {
-    return mats[x].m != mats[y].m ? mats[x].m > mats[y].m : mats[x].n > mats[y].n;
+    const int64_t a = mats[x].m * mats[x].n, b = mats[y].m * mats[y].n;
+    return a != b ? a > b : mats[x].m > mats[y].m;
   });
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -121,6 +197,15 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
     }
     ++p.shapes.back().count;
   }
+  p.count_off = take(sizeof(uint32_t) * kNsCounts);
+  size_t part = 0;
+  for (NsEpi epi : {kNsGram, kNsPoly, kNsApply})
+    for (int n = 1; n <= 2; ++n)
+      (void)ns_launches(p, NsLaunch{}, epi, n, [&](const NsLaunch&, const Cut16& c, int tile) {
+        part = std::max(part, cut_bytes(c, tile));
+        return hipSuccess;
+      });
+  p.part_off = take(part);
   p.bytes = off;
 }
 
@@ -163,66 +248,12 @@ bool ns_scales(const float* coeffs, int steps, std::vector<NsIter>& it) {
   return true;
 }
 
-// One grouped launch per kNsMaxClasses shapes; planes: 0 for all shapes, else
-// those with that many planes.
-template <class Fill, class Go>
-hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, int planes, Fill fill, Go go) {
-  NsLaunch L = base;
-  L.nclass = 0;
-  L.total = 0;
-  for (const NsClass& s : p.shapes) {
-    if (planes != 0 && s.planes != planes) continue;
-    NsClass c = s;
-    fill(p.table[s.first], c);
-    c.base = L.total;
-    L.cls[L.nclass++] = c;
-    L.total += c.count * c.tiles;
-    if (L.nclass == kNsMaxClasses) {
-      const hipError_t e = go(L);
-      if (e != hipSuccess) return e;
-      L.nclass = 0;
-      L.total = 0;
-    }
-  }
-  return L.nclass > 0 ? go(L) : hipSuccess;
-}
-
-#define NS_TRY(expr)              \
-  do {                            \
-    const hipError_t e_ = (expr); \
-    if (e_ != hipSuccess) return e_; \
-  } while (0)
-
-hipError_t ns_product(const NsPlan& p, const NsLaunch& base, NsEpi epi, hipStream_t st) {
-  const bool sym = epi == kNsGram || epi == kNsGramPoly || epi == kNsPoly;
-  auto shape = [&](int tile) {
-    return [=](const NsDesc& d, NsClass& c) {
-      c.tx = static_cast<int32_t>(ns_cdiv(ns_pad(d.p), tile));
-      c.ty = sym ? c.tx : static_cast<int32_t>(ns_cdiv(ns_pad(d.q), tile));
-      c.tiles = sym ? ns_sym_items(c.tx) : c.tx * c.ty;
-    };
-  };
-  for (int planes = 1; planes <= 2; ++planes) {
-    // 256 x 256 tiles where they fill the chip (one workgroup per CU)
-    int64_t big = 0;
-    for (const NsClass& s : p.shapes) {
-      if (s.planes != planes) continue;
-      NsClass c = s;
-      shape(256)(p.table[s.first], c);
-      big += static_cast<int64_t>(c.tiles) * c.count;
-    }
-    if (big == 0) continue;
-    const int tile = big >= 256 ? 256 : 128;
-    NS_TRY(ns_grouped(p, base, planes, shape(tile),
-                      [&](const NsLaunch& L) { return launch_ns_product(L, epi, planes, tile, st); }));
-  }
-  return hipSuccess;
-}
-
 hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool step,
                       char* ws, hipStream_t st) {
   L.ws = ws;
   L.status = reinterpret_cast<int32_t*>(ws + p.status_off);
+  L.count = reinterpret_cast<uint32_t*>(ws + p.count_off);
+  L.part = reinterpret_cast<float*>(ws + p.part_off);
   const int count = static_cast<int>(p.table.size());
   if (count == 1) {
     L.inl = p.table[0];

@@ -9,6 +9,7 @@ namespace dion {
 constexpr int kNsPad = 64;        // rows and columns of every plane are padded to this, with zeros
 constexpr int kNsParts = 512;     // most partial sums of squares per matrix
 constexpr int kNsMaxClasses = 8;
+constexpr int kNsCounts = 512;    // arrival counters of cut tiles (at most the chip's workgroup slots)
 constexpr int kNsUpload = 24;     // descriptors per table upload (kernel arguments: under 4 KB)
 constexpr int32_t kNsNonFinite = 8;   // status bit: DION_STATUS_NONFINITE
 inline __host__ __device__ int64_t ns_pad(int64_t x) { return (x + kNsPad - 1) / kNsPad * kNsPad; }
@@ -75,6 +76,9 @@ struct NsLaunch {
   int32_t tau;            // f_acc is multiplied by tau^this (first iteration)
   int32_t src;            // which of the two X buffers is read
   int32_t gdtype, odtype; // 0 float32, 1 bfloat16
+  int32_t full, slices;   // mm16.h, Work16 (total counts tiles)
+  float* part;
+  uint32_t* count;
 };
 
 struct NsUpload {
@@ -87,8 +91,8 @@ hipError_t launch_ns_table(const NsUpload& u, hipStream_t st);
 hipError_t launch_ns_norm(const NsLaunch& L, hipStream_t st);
 hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st);
 // tile: 128 or 256
-hipError_t launch_ns_product(const NsLaunch& L, NsEpi epi, int planes, int tile, hipStream_t st);
-// work items of a symmetric product over an nt x nt tile grid
-int ns_sym_items(int nt);
+hipError_t launch_ns_product(const NsLaunch& L, int items, NsEpi epi, int planes, int tile, hipStream_t st);
+// tiles of a symmetric product over an nt x nt tile grid
+inline int ns_sym_tiles(int nt) { return nt * (nt + 1) / 2; }
 
 }  // namespace dion

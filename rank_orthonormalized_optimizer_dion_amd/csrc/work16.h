@@ -1,0 +1,41 @@
+// How many workgroups a product's tiles take (host side of mm16.h's Work16).
+#pragma once
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+namespace dion {
+
+constexpr int kTileSlots256 = 256;   // one workgroup of 256 x 256 tiles per CU
+constexpr int kTileSlots128 = 512;   // two of 128 x 128 tiles
+inline int tile_slots(int tile) { return tile == 256 ? kTileSlots256 : kTileSlots128; }
+
+// Reductions shorter than this are not cut: joining would cost what it saves.
+constexpr int64_t kMinCutStages = 40;
+
+struct Cut16 {
+  int64_t full;    // tiles of one workgroup each
+  int64_t cut;     // tiles cut into `slices`
+  int64_t slices;
+  int64_t items() const { return full + cut * slices; }
+};
+
+// `stages`: reduction stages (mm16.h) per tile.  The last round of tiles is
+// cut until it fills the chip's slots, but not beyond sqrt(0.4 stages) slices:
+// adding up one slice's sums (a tile of float32 through one workgroup) takes
+// as long as about 2.5 stages.
+inline Cut16 cut_tiles(int64_t tiles, int tile, int64_t stages) {
+  if (stages < kMinCutStages) return {tiles, 0, 1};
+  const int64_t slots = tile_slots(tile);
+  const int64_t full = tiles / slots * slots, rest = tiles - full;
+  if (rest == 0) return {tiles, 0, 1};
+  const int64_t most = static_cast<int64_t>(std::sqrt(0.4 * static_cast<double>(stages)));
+  const int64_t slices = std::max<int64_t>(1, std::min(slots / rest, most));
+  if (slices == 1) return {tiles, 0, 1};
+  return {full, rest, slices};
+}
+inline size_t cut_bytes(const Cut16& c, int tile) {
+  return static_cast<size_t>(c.cut * c.slices) * tile * tile * 4;
+}
+
+}  // namespace dion
