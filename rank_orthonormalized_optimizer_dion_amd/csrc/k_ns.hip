@@ -15,47 +15,18 @@
 // (N(0, 1) matrices), at the same matrix rate.  Two planes (hi + lo, 22
 // bits) give float32's accuracy at a third of the rate.
 #include "mm16.h"
+#include "ns_device.h"
 #include "ns_types.h"
 
 namespace dion {
 
 namespace {
 
-__device__ __forceinline__ void ns_locate(const NsLaunch& L, int t, NsDesc& d, NsClass& c, int& local) {
-  c = L.cls[0];
-#pragma unroll
-  for (int i = 1; i < kNsMaxClasses; ++i)
-    if (i < L.nclass && t >= L.cls[i].base) c = L.cls[i];
-  const int rel = t - c.base;
-  const int mi = rel / c.tiles;
-  local = rel - mi * c.tiles;
-  d = L.table ? L.table[c.first + mi] : L.inl;
-}
-
 __global__ __launch_bounds__(256) void k_ns_table(NsUpload u) {
   const int words = u.count * static_cast<int>(sizeof(NsDesc) / 4);
   const uint32_t* src = reinterpret_cast<const uint32_t*>(u.d);
   uint32_t* dst = reinterpret_cast<uint32_t*>(u.dst);
   for (int i = threadIdx.x; i < words; i += 256) dst[i] = src[i];
-}
-
-template <typename GT>
-__device__ __forceinline__ float load_g(const void* G, int64_t o) {
-  if constexpr (sizeof(GT) == 2) return bf16_to_f32(static_cast<const uint16_t*>(G)[o]);
-  else return static_cast<const float*>(G)[o];
-}
-
-// The new momentum and the matrix to orthogonalize, each one rounding per
-// operation, the same in both kernels that form them.
-__device__ __forceinline__ float ns_moment(const NsLaunch& L, float g, float m) { return fmaf(L.mu, m, g); }
-__device__ __forceinline__ float ns_dir(const NsLaunch& L, float g, float m1) {
-  return L.nesterov ? fmaf(L.mu, m1, g) : m1;
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-  return v;
 }
 
 // Partial sums of squares of D over `chunk` elements each, in float64 (a

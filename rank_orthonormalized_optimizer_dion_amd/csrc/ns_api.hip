@@ -74,15 +74,24 @@ int ns_validate(const NsMatrix& a, int gdtype, int odtype, bool step) {
   return DION_OK;
 }
 
-// One grouped launch per kNsMaxClasses shapes; planes: 0 for all shapes, else
-// those with that many planes.
-template <class Fill, class Go>
-hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, int planes, Fill fill, Go go) {
+// Whether a p x q matrix (p <= q) takes the one-workgroup form, and the
+// padded sides it takes it with: X's planes and one p x p plane have to fit
+// 160 KB of LDS.
+bool ns_small(int p, int q, int& spp, int& sqp) {
+  spp = p <= 64 ? 64 : 128;
+  sqp = q <= 128 ? 128 : q <= 256 ? 256 : 512;
+  return p <= 128 && q <= (p <= 64 ? 512 : 256);
+}
+
+// One grouped launch per kNsMaxClasses shapes; the shapes are those that
+// `pick` accepts.
+template <class Pick, class Fill, class Go>
+hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, Pick pick, Fill fill, Go go) {
   NsLaunch L = base;
   L.nclass = 0;
   L.total = 0;
   for (const NsClass& s : p.shapes) {
-    if (planes != 0 && s.planes != planes) continue;
+    if (!pick(s)) continue;
     NsClass c = s;
     fill(p.table[s.first], c);
     c.base = L.total;
@@ -128,7 +137,7 @@ hipError_t ns_launches(const NsPlan& p, const NsLaunch& base, NsEpi epi, int pla
   }
   if (big == 0) return hipSuccess;
   const int tile = big >= kNsBigTiles ? 256 : 128;
-  return ns_grouped(p, base, planes, shape(tile), [&](NsLaunch L) {
+  return ns_grouped(p, base, [=](const NsClass& s) { return s.planes == planes; }, shape(tile), [&](NsLaunch L) {
     const NsDesc& d = p.table[L.cls[L.nclass - 1].first];
     const int64_t k = ns_pad(epi == kNsGram || epi == kNsGramPoly ? d.q : d.p);
     const Cut16 c = cut_tiles(L.total, tile, k * planes / 32);
@@ -182,17 +191,23 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
     const int64_t total = a.m * a.n;
     d.chunk = std::max<int64_t>(8192, ns_cdiv(ns_cdiv(total, kNsParts), 1024) * 1024);
     d.parts = static_cast<int32_t>(ns_cdiv(total, d.chunk));
-    d.planes = d.p <= kNsSmallSide ? 2 : planes;
+    int spp, sqp;
+    const bool small = ns_small(d.p, d.q, spp, sqp);
+    d.planes = small ? 0 : d.p <= kNsSmallSide ? 2 : planes;
     const size_t row = 2 * d.planes * ns_pad(d.p);
-    d.oX = take(2 * row * ns_pitch(d.q, d.planes));
-    d.oA = take(row * ns_pitch(d.p, d.planes));
-    d.oB = take(row * ns_pitch(d.p, d.planes));
-    d.oS = take(kNsParts * 8 + 16);
+    if (!small) {
+      d.oX = take(2 * row * ns_pitch(d.q, d.planes));
+      d.oA = take(row * ns_pitch(d.p, d.planes));
+      d.oB = take(row * ns_pitch(d.p, d.planes));
+      d.oS = take(kNsParts * 8 + 16);
+    }
     p.table[g] = d;
     if (g == 0 || mats[order[g]].m != mats[order[g - 1]].m || mats[order[g]].n != mats[order[g - 1]].n) {
       NsClass c{};
       c.first = g;
       c.planes = d.planes;
+      c.spp = spp;
+      c.sqp = sqp;
       p.shapes.push_back(c);
     }
     ++p.shapes.back().count;
@@ -220,7 +235,6 @@ struct NsIter {
 // kept at 2^15 at most.  Returns false when the coefficients let singular
 // values grow past kNsMaxGrowth.
 constexpr double kNsMaxGrowth = 64.0;
-constexpr int kNsMaxSteps = 32;
 bool ns_scales(const float* coeffs, int steps, std::vector<NsIter>& it) {
   auto pow2_below = [](double bound) {   // the power of two that brings `bound` to 2^14..2^15
     return std::ldexp(1.0, 15 - static_cast<int>(std::ceil(std::log2(std::max(bound * 1.01, 1e-3)))));
@@ -248,6 +262,22 @@ bool ns_scales(const float* coeffs, int steps, std::vector<NsIter>& it) {
   return true;
 }
 
+NsSmall ns_small_args(const NsLaunch& L, const std::vector<NsIter>& it, bool step) {
+  NsSmall a{};
+  a.common = L;
+  a.common.x0 = static_cast<float>(it[0].sx);
+  a.steps = static_cast<int32_t>(it.size());
+  a.step = step;
+  for (size_t k = 0; k < it.size(); ++k) {
+    const NsIter& s = it[k];
+    const double next = k + 1 < it.size() ? it[k + 1].sx : 1.0;
+    a.it[k] = {static_cast<float>(s.sa / (s.sx * s.sx)), static_cast<float>(s.c * s.sb / (s.sa * s.sa)),
+               static_cast<float>(s.b * s.sb / s.sa), static_cast<float>(s.a * s.sb),
+               static_cast<float>(next / (s.sb * s.sx))};
+  }
+  return a;
+}
+
 hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool step,
                       char* ws, hipStream_t st) {
   L.ws = ws;
@@ -270,11 +300,18 @@ hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool
     }
     L.table = dst;
   }
-  NS_TRY(ns_grouped(p, L, 0, [](const NsDesc& d, NsClass& c) { c.tiles = d.parts; },
+  for (int v = 0; v < 5; ++v) {   // the one-workgroup forms
+    const int spp = v < 3 ? 64 : 128, sqp = v < 3 ? 128 << v : 128 << (v - 3);
+    NS_TRY(ns_grouped(p, L, [=](const NsClass& c) { return c.planes == 0 && c.spp == spp && c.sqp == sqp; },
+                      [](const NsDesc&, NsClass& c) { c.tiles = 1; },
+                      [&](const NsLaunch& K) { return launch_ns_small(ns_small_args(K, it, step), spp, sqp, st); }));
+  }
+  NS_TRY(ns_grouped(p, L, [](const NsClass& c) { return c.planes != 0; },
+                    [](const NsDesc& d, NsClass& c) { c.tiles = d.parts; },
                     [&](const NsLaunch& K) { return launch_ns_norm(K, st); }));
   L.x0 = static_cast<float>(it[0].sx);
   for (int planes = 1; planes <= 2; ++planes)
-    NS_TRY(ns_grouped(p, L, planes, [](const NsDesc& d, NsClass& c) {
+    NS_TRY(ns_grouped(p, L, [=](const NsClass& c) { return c.planes == planes; }, [](const NsDesc& d, NsClass& c) {
       c.tx = static_cast<int32_t>(ns_pad(d.p) / 64);
       c.ty = static_cast<int32_t>(ns_pad(d.q) / 64);
       c.tiles = c.tx * c.ty;

@@ -45,7 +45,8 @@ struct NsDesc {
 };
 
 struct NsClass {
-  int32_t planes;
+  int32_t planes;         // 0: the one-workgroup form
+  int32_t spp, sqp;       // its padded sides
   int32_t first, count;   // matrices of this shape in the table
   int32_t tiles, base;    // work items per matrix, first item
   int32_t tx, ty;         // tile grid
@@ -81,6 +82,17 @@ struct NsLaunch {
   uint32_t* count;
 };
 
+// The one-workgroup form (k_ns_small): every iteration's factors at once.
+constexpr int kNsMaxSteps = 32;
+struct NsSmall {
+  struct Iter {
+    float f_gram, f_acc, f_a, f_i, f_apply;   // f_acc = 0: no A^2 (cubic)
+  };
+  NsLaunch common;        // classes (tiles = 1), status, momentum, types
+  int32_t steps, step;    // step: Muon step, else the output is written
+  Iter it[kNsMaxSteps];
+};
+
 struct NsUpload {
   NsDesc d[kNsUpload];
   NsDesc* dst;
@@ -88,6 +100,8 @@ struct NsUpload {
 };
 
 hipError_t launch_ns_table(const NsUpload& u, hipStream_t st);
+// pp, qp: (64, 128), (64, 256), (64, 512), (128, 128) or (128, 256)
+hipError_t launch_ns_small(const NsSmall& L, int pp, int qp, hipStream_t st);
 hipError_t launch_ns_norm(const NsLaunch& L, hipStream_t st);
 hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st);
 // tile: 128 or 256

@@ -276,3 +276,49 @@ def test_muon_list_non_finite_and_zero(gpu_lib):
     assert rel(X[1], x) <= TOL32 and rel(M[1], mm) <= 2.0 ** -22
     assert rel(X[3], x0[3].double() * (1 - f32(0.02) * 0.5)) <= 2.0 ** -22
     assert torch.count_nonzero(M[3]) == 0
+
+
+# sides around the limits of the one-workgroup form (64 x 512, 128 x 256) and
+# the two-plane products of a short side
+LIMITS = [(64, 512), (64, 513), (65, 256), (65, 257), (128, 257), (100, 700), (17, 400), (512, 64), (257, 128),
+          (33, 129), (64, 129), (127, 128)]
+
+
+@pytest.mark.parametrize("m,n", LIMITS)
+def test_limits_of_the_schedules(gpu_lib, m, n):
+    import torch
+    say(f"ns limits {m}x{n}")
+    G = draw(m, n, 300 + m + n, torch.float32)
+    O = torch.full((m, n), float("nan"), device="cuda")
+    for cs in ([Q] * 5, [CUBIC] * 3, [Q, CUBIC]):
+        gpu_lib.orthogonalize(G, O, cs, len(cs), "f32")
+        assert rel(O, ns64(G.double(), cs)) <= TOL32
+    Ob = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.orthogonalize(G, Ob, Q, 5, "f16")
+    assert rel(Ob, ns64(G.double(), [Q] * 5)) <= TOL16 + TOL_BF
+
+
+@pytest.mark.parametrize("m,n", [(64, 513), (257, 129), (100, 700), (40, 500), (128, 200)])
+def test_muon_schedules(gpu_lib, m, n):
+    import torch
+    X, M = draw(m, n, 1, torch.float32) * 0.02, draw(m, n, 2, torch.float32)
+    G = draw(m, n, 3, torch.bfloat16)
+    x, mm = muon64(X.double(), G.double(), M.double(), 0.02, 0.95, True, 0.1, 1.5, [Q] * 5)
+    gpu_lib.muon_step(X, G, M, 0.02, 0.95, True, 0.1, 1.5, Q, 5)
+    assert rel(M, mm) <= 2.0 ** -22
+    bound = TOL32 * 0.02 * 1.5 * min(m, n) ** 0.5 * 1.2 + 2.0 ** -22 * float(torch.linalg.vector_norm(x))
+    assert float(torch.linalg.vector_norm(X.double() - x)) <= bound
+
+
+def test_large_reductions_are_cut(gpu_lib):
+    """Few tiles and a long reduction: the tiles' slices are joined; twice the
+    same bits."""
+    import torch
+    for m, n, mode, tol in ((300, 6000, "f16", TOL16), (6000, 300, "f32", TOL32), (1500, 1700, "f32", TOL32)):
+        say(f"ns cut {m}x{n} {mode}")
+        G = draw(m, n, m, torch.float32)
+        O, P = torch.empty_like(G), torch.empty_like(G)
+        gpu_lib.orthogonalize(G, O, math=mode)
+        gpu_lib.orthogonalize(G, P, math=mode)
+        assert rel(O, ns64(G.double(), [Q] * 5)) <= tol
+        assert torch.equal(O, P)
