@@ -471,30 +471,53 @@ def _check_rows(name, t, shape=None, dtypes=None, device=None):
     """A 2-D GPU tensor whose rows are contiguous; returns its row pitch."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 2:
+    got = t.shape
+    if len(got) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape is not None and got != shape:
+        raise ValueError(f"shape mismatch: {name} is {tuple(got)}, expected {tuple(shape)}")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    m, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    m, n = got
+    row, col = t.stride()
+    if n > 1 and col != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    pitch = t.stride(0) if m > 1 else n
+    pitch = row if m > 1 else n
     if pitch < n:
         raise ValueError(f"{name} must have rows that do not overlap")
     return pitch
 
 
-def _scratch(nbytes: int, device, workspace, stream):
-    """The caller's workspace, or a new one; a new one that another stream
-    than the current one will use is marked so for torch's allocator."""
-    ws = _workspace(nbytes, device, workspace)
-    if workspace is None and stream is not None:
-        ws.record_stream(stream)
-    return ws
+def _launch(size, run, device, workspace, stream):
+    """run(pointer, bytes, stream) on `device` with the caller's workspace, or
+    with a new one of size() bytes; returns the workspace.  A new one that
+    another stream than the current one uses is marked so for torch's
+    allocator."""
+    torch = _torch()
+    if workspace is None:
+        nbytes = size()
+        if nbytes == 0:
+            raise _err(ERR_INVALID_ARG)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        nbytes = workspace.numel() * workspace.element_size()
+    args = (workspace.data_ptr(), nbytes, _stream_handle(stream, device))
+    if torch.cuda.current_device() == device.index:
+        rc = run(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = run(*args)
+    if rc == ERR_WORKSPACE:
+        raise ValueError(f"workspace too small: need {size()} bytes, 16-byte aligned")
+    if rc != OK:
+        raise _err(rc)
+    return workspace
 
 
 def _same_dtype(tensors, name):
@@ -522,17 +545,12 @@ def orthogonalize_batched(mats: Sequence[Tuple], coeffs=NS_COEFFS, steps: int = 
         arr[i] = dion_ns_matrix(G.data_ptr(), O.data_ptr(), G.shape[0], G.shape[1], ldg, ldo)
     gd, od = _same_dtype([g for g, _ in mats], "G"), _same_dtype([o for _, o in mats], "O")
     mode, cf = _ns_math(math), _ns_coeffs(coeffs, steps)
-    lib = load()
-    nbytes = lib.dion_orthogonalize_workspace_size(arr, len(mats), mode)
-    if nbytes == 0:
-        raise _err(ERR_INVALID_ARG)
-    ws = _scratch(nbytes, dev, workspace, stream)
-    with torch.cuda.device(dev):
-        rc = lib.dion_orthogonalize_batched(arr, len(mats), cf, int(steps), mode, gd, od,
-                                            ws.data_ptr(), nbytes, _stream_handle(stream, dev))
-    if rc != OK:
-        raise _err(rc)
-    return ws
+    lib, count = load(), len(mats)
+    return _launch(
+        lambda: lib.dion_orthogonalize_workspace_size(arr, count, mode),
+        lambda ws, nbytes, st: lib.dion_orthogonalize_batched(arr, count, cf, int(steps), mode, gd, od,
+                                                              ws, nbytes, st),
+        dev, workspace, stream)
 
 
 def orthogonalize(G, O, coeffs=NS_COEFFS, steps: int = 5, math="f32", workspace=None, stream=None):
@@ -575,18 +593,13 @@ def muon_step_batched(mats: Sequence[Tuple], lr: float, momentum: float = 0.95,
                                   _muon_scale(scale, m, n) if m and n else 0.0)
     gd = _same_dtype([g for _, g, _ in mats], "G")
     mode, cf = _ns_math(math), _ns_coeffs(coeffs, steps)
-    lib = load()
-    nbytes = lib.dion_muon_workspace_size(arr, len(mats), mode)
-    if nbytes == 0:
-        raise _err(ERR_INVALID_ARG)
-    ws = _scratch(nbytes, dev, workspace, stream)
-    with torch.cuda.device(dev):
-        rc = lib.dion_muon_step_batched(arr, len(mats), float(lr), float(momentum),
-                                        1 if nesterov else 0, float(weight_decay), cf, int(steps),
-                                        mode, gd, ws.data_ptr(), nbytes, _stream_handle(stream, dev))
-    if rc != OK:
-        raise _err(rc)
-    return ws
+    lib, count = load(), len(mats)
+    return _launch(
+        lambda: lib.dion_muon_workspace_size(arr, count, mode),
+        lambda ws, nbytes, st: lib.dion_muon_step_batched(
+            arr, count, float(lr), float(momentum), 1 if nesterov else 0, float(weight_decay), cf,
+            int(steps), mode, gd, ws, nbytes, st),
+        dev, workspace, stream)
 
 
 def muon_step(X, G, M, lr: float, momentum: float = 0.95, nesterov: bool = True,
@@ -626,17 +639,11 @@ def _put_vector(s, name, tensor, n, device):
 
 
 def _linear(name, s, device, workspace, stream):
-    lib = load()
-    size = getattr(lib, f"dion_linear_{name}_workspace_size")(ctypes.byref(s))
-    if size == 0:
-        raise _err(ERR_INVALID_ARG)
-    ws = _scratch(size, device, workspace, stream)
-    with _torch().cuda.device(device):
-        rc = getattr(lib, f"dion_linear_{name}")(ctypes.byref(s), ws.data_ptr(), size,
-                                                 _stream_handle(stream, device))
-    if rc != OK:
-        raise _err(rc)
-    return ws
+    lib, ref = load(), ctypes.byref(s)
+    size = getattr(lib, f"dion_linear_{name}_workspace_size")
+    run = getattr(lib, f"dion_linear_{name}")
+    return _launch(lambda: size(ref), lambda ws, nbytes, st: run(ref, ws, nbytes, st), device,
+                   workspace, stream)
 
 
 def _linear_dtype(t, name) -> int:

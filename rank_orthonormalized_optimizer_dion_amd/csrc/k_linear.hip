@@ -188,31 +188,28 @@ __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
       });
 }
 
-__global__ __launch_bounds__(256) void k_lin_zero(uint32_t* count, int n) {
-  for (int i = threadIdx.x; i < n; i += 256) count[i] = 0;
-}
-
-// dz = src act'(z) (or src itself) as planes with the columns past `cols`
-// zero, and its column sums over this workgroup's `chunk` rows.  256
-// columns by 8 row lanes per workgroup.
-__global__ __launch_bounds__(256) void k_lin_pack(LinPack p) {
-  __shared__ float red[8][256 + 8];
-  const int col = (blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
+// dz = src act'(z) (or src itself) as planes, zero past its columns and rows,
+// and its column sums over this workgroup's `chunk` rows.  256 columns by 8
+// row lanes per workgroup.
+__device__ __forceinline__ void pack_block(const LinPack& p, int block, float (&red)[8][256 + 8]) {
+  const int bx = block % p.gx, by = block / p.gx;
+  const int col = (bx * 32 + (threadIdx.x & 31)) * 8;
   const int lane = threadIdx.x >> 5;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.chunk;
-  const int64_t r1 = min(p.rows, r0 + p.chunk);
+  const int64_t r0 = static_cast<int64_t>(by) * p.chunk;
+  const int64_t r1 = min(p.prows, r0 + p.chunk);
   const bool vs = aligned16(p.src, p.ld, p.dtype), vz = aligned16(p.z, p.ldz, p.dtype);
   const int left = p.cols - col;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (col < (p.dst ? p.pitch : p.cols)) {
     for (int64_t r = r0 + lane; r < r1; r += 8) {
+      const int in = r < p.rows ? left : 0;   // rows past the last are zero
       float v[8];
-      load8(p.src, r * p.ld + col, p.dtype, vs, left, v);
+      load8(p.src, r * p.ld + col, p.dtype, vs, in, v);
       if (p.z) {
         float z[8];
-        load8(p.z, r * p.ldz + col, p.dtype, vz, left, z);
+        load8(p.z, r * p.ldz + col, p.dtype, vz, in, z);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= k < left ? act_slope(z[k], p.act) : 0.0f;
+        for (int k = 0; k < 8; ++k) v[k] *= k < in ? act_slope(z[k], p.act) : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum[k] += v[k];
@@ -236,21 +233,44 @@ __global__ __launch_bounds__(256) void k_lin_pack(LinPack p) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) red[lane][(threadIdx.x & 31) * 8 + k] = sum[k];
   __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  const int c = bx * 256 + threadIdx.x;
   if (c < p.cols) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    p.sums[static_cast<int64_t>(blockIdx.y) * p.cols + c] = s;
+    p.sums[static_cast<int64_t>(by) * p.cols + c] = s;
   }
 }
 
+__global__ __launch_bounds__(256) void k_lin_pack(LinPacks a) {
+  __shared__ float red[8][256 + 8];
+  int b = blockIdx.x;
+  if (b == 0)
+    for (int i = threadIdx.x; i < a.counts; i += 256) a.count[i] = 0;
+#pragma unroll
+  for (int i = 0; i < kLinPacks; ++i) {
+    if (i < a.n && b >= 0 && b < a.p[i].blocks) pack_block(a.p[i], b, red);
+    b -= i < a.n ? a.p[i].blocks : 0;
+  }
+}
+
+// The sum of the chunks' column sums: 32 columns by 8 lanes of chunks.
 __global__ __launch_bounds__(256) void k_lin_colsum(const float* part, int chunks, int n, float* out,
                                                     int accumulate) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
+  __shared__ float red[8][32];
+  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + col;
   float s = 0.0f;
-  for (int i = 0; i < chunks; ++i) s += part[static_cast<int64_t>(i) * n + c];
+  if (c < n) {
+#pragma unroll 8
+    for (int i = lane; i < chunks; i += 8) s += part[static_cast<int64_t>(i) * n + c];
+  }
+  red[lane][col] = s;
+  __syncthreads();
+  if (lane != 0 || c >= n) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += red[i][col];
   out[c] = accumulate ? out[c] + s : s;
 }
 
@@ -419,20 +439,15 @@ hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipSt
   return tile == 256 ? product<256>(p, kind, st) : product<128>(p, kind, st);
 }
 
-hipError_t launch_lin_zero(uint32_t* count, int n, hipStream_t st) {
-  k_lin_zero<<<dim3(1), dim3(256), 0, st>>>(count, n);
-  return hipGetLastError();
-}
-
-hipError_t launch_lin_pack(const LinPack& p, hipStream_t st) {
-  const int64_t width = p.dst ? p.pitch : p.cols;
-  const dim3 grid(static_cast<unsigned>((width + 255) / 256), static_cast<unsigned>((p.rows + p.chunk - 1) / p.chunk));
-  k_lin_pack<<<grid, dim3(256), 0, st>>>(p);
+hipError_t launch_lin_packs(const LinPacks& p, hipStream_t st) {
+  int blocks = 0;
+  for (int i = 0; i < p.n; ++i) blocks += p.p[i].blocks;
+  k_lin_pack<<<dim3(blocks > 0 ? blocks : 1), dim3(256), 0, st>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_lin_colsum(const float* part, int chunks, int n, float* out, int accumulate, hipStream_t st) {
-  k_lin_colsum<<<dim3((n + 255) / 256), dim3(256), 0, st>>>(part, chunks, n, out, accumulate);
+  k_lin_colsum<<<dim3((n + 31) / 32), dim3(256), 0, st>>>(part, chunks, n, out, accumulate);
   return hipGetLastError();
 }
 

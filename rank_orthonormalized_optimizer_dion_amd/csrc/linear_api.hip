@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "dion.h"
 #include "linear_types.h"
@@ -136,16 +137,19 @@ struct Run {
   Arena ws;
   bool go;   // false: only size the workspace
   hipStream_t st;
+  LinPacks packs;
 };
 
-// A padded copy of `s` (times act'(z) when z is given) in `planes` planes,
-// and on request its column sums.
-hipError_t lin_pack(Run& r, const Span& s, int planes, const Span* z, int act, bool copy, float* db, int accumulate,
-                    Operand& out) {
+constexpr int kLinStage = 32;   // k of a reduction stage (mm16.h)
+
+// Adds a padded copy of `s` (times act'(z) when z is given) in `planes`
+// planes to the call's copies, and on request its column sums.
+void lin_pack(Run& r, const Span& s, int planes, const Span* z, int act, bool copy, bool sums, Operand& out) {
   LinPack p{};
   p.src = s.p;
   p.ld = s.ld;
   p.rows = s.rows;
+  p.prows = copy ? lin_cdiv(s.rows, kLinStage) * kLinStage : s.rows;
   p.cols = static_cast<int32_t>(s.cols);
   p.dtype = s.esize == 2;
   p.planes = planes;
@@ -155,35 +159,40 @@ hipError_t lin_pack(Run& r, const Span& s, int planes, const Span* z, int act, b
     p.ldz = z->ld;
   }
   // at most 256 rows of partial sums
-  p.chunk = static_cast<int32_t>(std::max<int64_t>(32, lin_cdiv(lin_cdiv(s.rows, 256), 8) * 8));
-  const int chunks = static_cast<int>(lin_cdiv(s.rows, p.chunk));
+  p.chunk = static_cast<int32_t>(std::max<int64_t>(16, lin_cdiv(lin_cdiv(p.prows, 256), 8) * 8));
+  const int64_t chunks = lin_cdiv(p.prows, p.chunk);
   if (copy) {
     p.pitch = lin_cdiv(s.cols, 64) * 64;
-    p.plane = s.rows * p.pitch;
-    p.dst = r.ws.take<uint16_t>(static_cast<size_t>(p.planes) * p.plane);
+    p.plane = p.prows * p.pitch;
+    p.dst = r.ws.take<uint16_t>(static_cast<size_t>(planes) * p.plane);
     out = {p.dst, p.pitch, p.plane};
   }
-  if (db) p.sums = r.ws.take<float>(static_cast<size_t>(chunks) * s.cols);
-  if (!r.go) return hipSuccess;
-  if (s.rows > 0) LIN_TRY(launch_lin_pack(p, r.st));
-  if (db) LIN_TRY(launch_lin_colsum(p.sums, chunks, p.cols, db, accumulate, r.st));
-  return hipSuccess;
+  if (sums) p.sums = r.ws.take<float>(static_cast<size_t>(chunks) * s.cols);
+  p.gx = static_cast<int32_t>(lin_cdiv(copy ? p.pitch : s.cols, 256));
+  p.blocks = static_cast<int32_t>(p.gx * chunks);
+  r.packs.p[r.packs.n++] = p;
 }
 
-hipError_t lin_operand(Run& r, const Span& s, Operand& out) {
-  if (lin_direct(s)) {
-    out = {static_cast<const uint16_t*>(s.p), s.ld, 0};
-    return hipSuccess;
-  }
-  return lin_pack(r, s, s.esize == 2 ? 1 : 3, nullptr, DION_ACT_NONE, true, nullptr, 0, out);
+void lin_operand(Run& r, const Span& s, Operand& out) {
+  if (lin_direct(s)) out = {static_cast<const uint16_t*>(s.p), s.ld, 0};
+  else lin_pack(r, s, s.esize == 2 ? 1 : 3, nullptr, DION_ACT_NONE, true, false, out);
 }
 
-// A K-major operand's columns from K to the next multiple of 8 are zero (K
-// is one already for a tensor read in place, and a copy is padded); an
-// x-major operand's rows past K are not read.
-hipError_t lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K,
-                       int nseg, LinKind kind, const LinOut& out) {
-  LinProduct p{};
+// One product's launch.  A K-major operand's columns from K to the next
+// multiple of 8 are zero (K is one already for a tensor read in place, and a
+// copy is padded); an x-major operand's rows past K are not read.  padded:
+// both operands are copies, zero to the end of K's last stage.
+struct Product {
+  LinProduct p;
+  LinKind kind;
+  int tile;
+};
+Product lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, bool padded,
+                    int nseg, LinKind kind, const LinOut& out) {
+  Product f{};
+  LinProduct& p = f.p;
+  f.kind = kind;
+  if (padded) K = lin_cdiv(K, kLinStage) * kLinStage;
   p.a = a.p;
   p.b = b.p;
   p.lda = a.ld;
@@ -196,20 +205,27 @@ hipError_t lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, in
   p.nseg = nseg;
   p.out = out;
   // 256 x 256 tiles where they fill the chip
-  const int tile = lin_cdiv(M, 256) * lin_cdiv(N, 256) >= kLinBigTiles ? 256 : 128;
-  p.tx = static_cast<int32_t>(lin_cdiv(M, tile));
-  p.ty = static_cast<int32_t>(lin_cdiv(N, tile));
-  const Cut16 c = cut_tiles(static_cast<int64_t>(p.tx) * p.ty, tile, lin_cdiv(K, 32) * nseg);
+  f.tile = lin_cdiv(M, 256) * lin_cdiv(N, 256) >= kLinBigTiles ? 256 : 128;
+  p.tx = static_cast<int32_t>(lin_cdiv(M, f.tile));
+  p.ty = static_cast<int32_t>(lin_cdiv(N, f.tile));
+  const Cut16 c = cut_tiles(static_cast<int64_t>(p.tx) * p.ty, f.tile, lin_cdiv(K, kLinStage) * nseg);
   p.items = static_cast<int32_t>(c.items());
   p.full = static_cast<int32_t>(c.full);
   p.slices = static_cast<int32_t>(c.slices);
   if (c.cut) {
-    p.part = r.ws.take<float>(cut_bytes(c, tile) / 4);
-    p.count = r.ws.take<uint32_t>(c.cut);
+    p.part = r.ws.take<float>(cut_bytes(c, f.tile) / 4);
+    p.count = r.packs.count;   // shared by the call's products: all zero between launches
+    r.packs.counts = kTileSlots128;
   }
-  if (!r.go) return hipSuccess;
-  if (c.cut) LIN_TRY(launch_lin_zero(p.count, static_cast<int>(c.cut), r.st));
-  return launch_lin_product(p, kind, tile, r.st);
+  return f;
+}
+
+// The copies (and counters) a call's products need, then the products.
+hipError_t lin_enqueue(Run& r, std::initializer_list<const Product*> products) {
+  if (r.packs.n > 0 || r.packs.counts > 0) LIN_TRY(launch_lin_packs(r.packs, r.st));
+  for (const Product* f : products)
+    if (f->p.items > 0) LIN_TRY(launch_lin_product(f->p, f->kind, f->tile, r.st));
+  return hipSuccess;
 }
 
 hipError_t lin_forward(Run& r, const LinCall& c) {
@@ -237,9 +253,11 @@ hipError_t lin_forward(Run& r, const LinCall& c) {
     return r.go ? launch_lin_rows(s, vec, r.st) : hipSuccess;
   }
   Operand x, w;
-  LIN_TRY(lin_operand(r, c.x, x));
-  LIN_TRY(lin_operand(r, c.w, w));
-  return lin_product(r, x, w, l.t, l.n, l.k, f32 ? 6 : 1, kLinForward, out);
+  lin_operand(r, c.x, x);
+  lin_operand(r, c.w, w);
+  const bool padded = !lin_direct(c.x) && !lin_direct(c.w);
+  const Product y = lin_product(r, x, w, l.t, l.n, l.k, padded, f32 ? 6 : 1, kLinForward, out);
+  return r.go ? lin_enqueue(r, {&y}) : hipSuccess;
 }
 
 hipError_t lin_backward(Run& r, const LinCall& c) {
@@ -250,24 +268,29 @@ hipError_t lin_backward(Run& r, const LinCall& c) {
   const bool copy = products && (act || !lin_direct(c.dy));
   const int planes = f32 ? 3 : act && l.t <= kLinFewTokens ? 2 : 1;
   const int nseg = f32 ? 6 : planes;
-  if (copy || l.db)
-    LIN_TRY(lin_pack(r, c.dy, planes, act ? &c.z : nullptr, l.act, copy, l.db, l.accumulate, dz));
+  if (copy || l.db) lin_pack(r, c.dy, planes, act ? &c.z : nullptr, l.act, copy, l.db != nullptr, dz);
+  const LinPack sums = r.packs.p[0];
   if (products && !copy) dz = {static_cast<const uint16_t*>(l.dy), l.lddy, 0};
   LinOut out{};
   out.dtype = !f32;
+  Product dx{}, dw{};
   if (l.dx && l.t > 0) {
-    LIN_TRY(lin_operand(r, c.w, w));
+    lin_operand(r, c.w, w);
     out.y = l.dx;
     out.ldy = l.lddx;
-    LIN_TRY(lin_product(r, dz, w, l.t, l.k, l.n, nseg, kLinDx, out));
+    dx = lin_product(r, dz, w, l.t, l.k, l.n, copy && !lin_direct(c.w), nseg, kLinDx, out);
   }
   if (l.dw) {
-    if (l.t > 0) LIN_TRY(lin_operand(r, c.x, x));
+    if (l.t > 0) lin_operand(r, c.x, x);
     out.y = l.dw;
     out.ldy = l.lddw;
     out.accumulate = l.accumulate != 0;
-    LIN_TRY(lin_product(r, dz, x, l.n, l.k, l.t, nseg, kLinDw, out));
+    dw = lin_product(r, dz, x, l.n, l.k, l.t, copy && !lin_direct(c.x), nseg, kLinDw, out);
   }
+  if (!r.go) return hipSuccess;
+  LIN_TRY(lin_enqueue(r, {&dx, &dw}));
+  if (l.db)
+    LIN_TRY(launch_lin_colsum(sums.sums, sums.blocks / sums.gx, sums.cols, l.db, l.accumulate, r.st));
   return hipSuccess;
 }
 
@@ -275,21 +298,25 @@ template <class Check, class Go>
 size_t lin_size(const dion_linear* l, Check check, Go go) {
   LinCall c;
   if (!check(l, c)) return 0;
-  Run r{{nullptr}, false, nullptr};
+  Run r{{nullptr}, false, nullptr, {}};
+  r.packs.count = r.ws.take<uint32_t>(kTileSlots128);
   (void)go(r, c);
-  return r.ws.used + 256;   // a valid query is never 0
+  return r.ws.used;
 }
 
 template <class Check, class Go>
 int lin_run(const dion_linear* l, void* workspace, size_t bytes, void* stream, Check check, Go go) {
   LinCall c;
   if (!check(l, c)) return DION_ERR_INVALID_ARG;
-  Run size{{nullptr}, false, nullptr};
+  Run size{{nullptr}, false, nullptr, {}};
+  size.packs.count = size.ws.take<uint32_t>(kTileSlots128);
+  const size_t counters = size.ws.used;
   (void)go(size, c);
-  if (size.ws.used > 0 &&
-      (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0 || bytes < size.ws.used))
+  const bool needed = size.packs.counts > 0 || size.ws.used > counters;
+  if (needed && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0 || bytes < size.ws.used))
     return DION_ERR_WORKSPACE;
-  Run r{{static_cast<char*>(workspace)}, true, static_cast<hipStream_t>(stream)};
+  Run r{{static_cast<char*>(workspace)}, true, static_cast<hipStream_t>(stream), {}};
+  r.packs.count = r.ws.take<uint32_t>(kTileSlots128);
   return go(r, c) == hipSuccess ? DION_OK : DION_ERR_HIP;
 }
 

@@ -47,12 +47,23 @@ struct LinPack {
   int64_t ld;
   const void* z;        // pre-activation (dz = src act'(z)), or null
   int64_t ldz;
-  uint16_t* dst;        // planes, pitch `pitch` >= cols, zero past cols; or null
+  uint16_t* dst;        // planes, pitch `pitch` >= cols, zero past cols and rows; or null
   int64_t pitch, plane;
   float* sums;          // partial column sums, one row per chunk; or null
   int64_t rows;
+  int64_t prows;        // rows of the planes: `rows` up to a whole reduction stage
   int32_t cols, chunk;  // rows per workgroup
   int32_t act, dtype, planes;
+  int32_t gx, blocks;   // workgroups across the columns, and in all
+};
+
+// Up to three copies in one launch, which also clears the arrival counters
+// of the products that follow.
+constexpr int kLinPacks = 3;
+struct LinPacks {
+  LinPack p[kLinPacks];
+  uint32_t* count;
+  int32_t n, counts;
 };
 
 struct LinSkinny {
@@ -67,8 +78,7 @@ constexpr int kSkinnyTokens = 64;   // matrix-core kernel for few tokens
 constexpr int kRowTokens = 8;       // float32 / unaligned kernel for few tokens
 
 hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st);
-hipError_t launch_lin_zero(uint32_t* count, int n, hipStream_t st);
-hipError_t launch_lin_pack(const LinPack& p, hipStream_t st);
+hipError_t launch_lin_packs(const LinPacks& p, hipStream_t st);
 hipError_t launch_lin_colsum(const float* part, int chunks, int n, float* out, int accumulate,
                              hipStream_t st);
 hipError_t launch_lin_skinny(const LinSkinny& p, hipStream_t st);
