@@ -14,6 +14,7 @@
 #include "dion.h"
 #include "linear_types.h"
 #include "mm16.h"
+#include "work16.h"
 
 namespace dion {
 
@@ -148,12 +149,12 @@ __device__ __forceinline__ void six_pairs(int s, int& a, int& b) {
   }
 }
 
-template <int TILE, LinKind KIND>
-using LinShape = Shape16<B16, TILE, TILE, TILE / 64, 2, 1, KIND == kLinDw, KIND != kLinForward>;
+template <int TILE, int ST, LinKind KIND>
+using LinShape = Shape16<B16, TILE, TILE, TILE / 64, 2, ST, 1, KIND == kLinDw, KIND != kLinForward>;
 
-template <int TILE, LinKind KIND, int ACT>
+template <int TILE, int ST, LinKind KIND, int ACT>
 __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
-  using S = LinShape<TILE, KIND>;
+  using S = LinShape<TILE, ST, KIND>;
   __shared__ u32x4 smem[S::LDS_CELLS];
   const Work16 work{p.full, p.slices, p.part, p.count};
   const Item16 it = item16(work, xcd_remap(blockIdx.x, gridDim.x));
@@ -401,22 +402,22 @@ __global__ __launch_bounds__(256) void k_lin_rows(LinSkinny p) {
     }
 }
 
-template <int TILE, LinKind KIND, int ACT>
+template <int TILE, int ST, LinKind KIND, int ACT>
 hipError_t product(const LinProduct& p, hipStream_t st) {
-  k_lin_mm<TILE, KIND, ACT><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p);
+  k_lin_mm<TILE, ST, KIND, ACT><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p);
   return hipGetLastError();
 }
 
-template <int TILE>
+template <int TILE, int ST>
 hipError_t product(const LinProduct& p, LinKind kind, hipStream_t st) {
-  if (kind == kLinDx) return product<TILE, kLinDx, DION_ACT_NONE>(p, st);
-  if (kind == kLinDw) return product<TILE, kLinDw, DION_ACT_NONE>(p, st);
+  if (kind == kLinDx) return product<TILE, ST, kLinDx, DION_ACT_NONE>(p, st);
+  if (kind == kLinDw) return product<TILE, ST, kLinDw, DION_ACT_NONE>(p, st);
   switch (p.out.act) {
-    case DION_ACT_RELU: return product<TILE, kLinForward, DION_ACT_RELU>(p, st);
-    case DION_ACT_RELU2: return product<TILE, kLinForward, DION_ACT_RELU2>(p, st);
-    case DION_ACT_GELU: return product<TILE, kLinForward, DION_ACT_GELU>(p, st);
-    case DION_ACT_SILU: return product<TILE, kLinForward, DION_ACT_SILU>(p, st);
-    default: return product<TILE, kLinForward, DION_ACT_NONE>(p, st);
+    case DION_ACT_RELU: return product<TILE, ST, kLinForward, DION_ACT_RELU>(p, st);
+    case DION_ACT_RELU2: return product<TILE, ST, kLinForward, DION_ACT_RELU2>(p, st);
+    case DION_ACT_GELU: return product<TILE, ST, kLinForward, DION_ACT_GELU>(p, st);
+    case DION_ACT_SILU: return product<TILE, ST, kLinForward, DION_ACT_SILU>(p, st);
+    default: return product<TILE, ST, kLinForward, DION_ACT_NONE>(p, st);
   }
 }
 
@@ -436,7 +437,8 @@ hipError_t rows(const LinSkinny& p, bool vec, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st) {
-  return tile == 256 ? product<256>(p, kind, st) : product<128>(p, kind, st);
+  if (tile == 256) return product<256, 4>(p, kind, st);
+  return p.items <= kTileSlots256 ? product<128, 8>(p, kind, st) : product<128, 4>(p, kind, st);
 }
 
 hipError_t launch_lin_packs(const LinPacks& p, hipStream_t st) {

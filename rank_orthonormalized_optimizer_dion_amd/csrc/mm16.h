@@ -73,7 +73,6 @@ static __device__ u32x4 g_zero_cell;
 // One LDS stage holds kStep16 16-bit values of the reduction per x: 32 k, or
 // 16 k as hi and lo.
 constexpr int kStep16 = 32;
-constexpr int kStages16 = 4;
 
 // One operand of a tile: its pitch (2 ld when PL = 2), the tile's first x,
 // the number of x and the reduction length K (K-major operands: the columns
@@ -160,11 +159,12 @@ struct Tile16 {
   }
 };
 
-// Shape of one tile product: BM x BN outputs, WM x WN wavefronts.
-template <class E_, int BM_, int BN_, int WM_, int WN_, int PL_, bool AMC_, bool BMC_>
+// Shape of one tile product: BM x BN outputs, WM x WN wavefronts, ST LDS
+// stages (a power of two).
+template <class E_, int BM_, int BN_, int WM_, int WN_, int ST_, int PL_, bool AMC_, bool BMC_>
 struct Shape16 {
   using E = E_;
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PL = PL_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, PL = PL_;
   static constexpr int NT = 64 * WM * WN;
   static constexpr int TM = BM / WM, TN = BN / WN;
   static constexpr int F = PL == 1 ? 16 : 32;            // side of a matrix instruction's output
@@ -177,7 +177,7 @@ struct Shape16 {
   // epilogue staging: one 64 x 64 block of floats per wavefront, rows padded by 4
   static constexpr int EPITCH = 68;
   static constexpr int ECELLS = WM * WN * 64 * EPITCH / 4;
-  static constexpr int LDS_CELLS = kStages16 * STAGE > ECELLS ? kStages16 * STAGE : ECELLS;
+  static constexpr int LDS_CELLS = ST * STAGE > ECELLS ? ST * STAGE : ECELLS;
   static_assert(TN % 64 == 0 && TM % 64 == 0, "the epilogue stages 64-wide blocks");
 };
 
@@ -245,21 +245,22 @@ __device__ __forceinline__ void interleave16() {
 
 // acc = sum over nseg segments and k in [kbeg, kend).
 //
-// Four LDS stages.  A step t runs two clusters of matrix instructions.
-// During the first it reads the rest of stage t's operands; then it meets the
-// other wavefronts (stage t + 1 has arrived; everybody is done with stage
-// t - 1); during the second it reads the first operands of stage t + 1 and
-// starts the loads of stage t + 3.  So loads have two steps to arrive, and a
-// wavefront always has a cluster whose operands are in registers when it
-// reaches the barrier.  Two wavefronts per SIMD (256 x 256 tiles) or two
-// workgroups per CU (128 x 128) fill each other's gaps.
+// A step t runs two clusters of matrix instructions.  During the first it
+// reads the rest of stage t's operands; then it meets the other wavefronts
+// (stage t + 1 has arrived; everybody is done with stage t - 1); during the
+// second it reads the first operands of stage t + 1 and starts the loads of
+// stage t + ST - 1.  So loads have ST - 2 steps to arrive, and a wavefront
+// always has a cluster whose operands are in registers when it reaches the
+// barrier.  Two wavefronts per SIMD (256 x 256 tiles, 4 stages) or two
+// workgroups per CU (128 x 128, 4 stages) fill each other's gaps; a launch
+// of too few 128 x 128 tiles for that takes 8 stages.
 // kend - kbeg is a multiple of a stage's k.
 template <class S, class Seg>
 __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typename S::B& tb,
                                           const Planes16& pl, int total, Seg seg, int kbeg,
                                           int kend, u32x4* smem, typename S::Acc (&acc)[S::FM][S::FN]) {
   int is = 0, ik = kbeg;   // segment and reduction offset of the next issue
-  auto stage = [&](int t) { return smem + (t & (kStages16 - 1)) * S::STAGE; };
+  auto stage = [&](int t) { return smem + (t & (S::ST - 1)) * S::STAGE; };
   auto issue = [&](int t) {
     int ia, ib;
     seg(is, ia, ib);
@@ -271,16 +272,12 @@ __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typenam
     ik = wrap ? kbeg : ik;
     is += wrap;
   };
-  issue(0);
-  if (total > 1) issue(1);
-  if (total > 2) issue(2);
-  if (total > 2) arrive16<2 * S::PER>();
-  else if (total > 1) arrive16<S::PER>();
+  constexpr int D = S::ST - 1;   // stages in flight
+#pragma unroll
+  for (int i = 0; i < D; ++i)
+    if (i < total) issue(i);
+  if (total >= D) arrive16<(D - 1) * S::PER>();
   else arrive16<0>();
-  auto arrive = [&](int t) {   // stage t + 1 is there
-    if (t + 2 < total) arrive16<S::PER>();
-    else arrive16<0>();
-  };
   constexpr int RA = S::A::READS, RB = S::B::READS;
   int t = 0;
   if constexpr (S::PL == 1) {
@@ -291,26 +288,33 @@ __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typenam
       load_a<S>(a1, stage(t), H, 0);
       mma16<S>(a0, b, 0, acc);
       interleave16<H * S::FN, H * RA, 0>();
-      arrive16<S::PER>();
+      arrive16<(D - 2) * S::PER>();
       load_a<S>(a0, stage(t + 1), 0, 0);
       load_b<S>(next, stage(t + 1), 0);
-      issue(t + 3);
+      issue(t + D);
       mma16<S>(a1, b, H, acc);
       interleave16<H * S::FN, H * RA + S::FN * RB, S::PER>();
     };
     load_a<S>(a0, smem, 0, 0);
     load_b<S>(b0, smem, 0);
-    for (; t < total - 4; t += 2) {
+    for (; t < total - D - 1; t += 2) {
       step(t, b0, b1);
       step(t + 1, b1, b0);
     }
-    for (; t < total; ++t) {
+    if (t < total - D) {
+      step(t, b0, b1);
+#pragma unroll
+      for (int n = 0; n < S::FN; ++n) b0[n] = b1[n];
+      ++t;
+    }
+    // every load has been started: one more meeting, then no barriers
+    for (bool met = false; t < total; ++t) {
       load_a<S>(a1, stage(t), H, 0);
       mma16<S>(a0, b0, 0, acc);
       mma16<S>(a1, b0, H, acc);
       if (t + 1 < total) {
-        arrive(t);
-        if (t + 3 < total) issue(t + 3);
+        if (!met) arrive16<0>();
+        met = true;
         load_a<S>(a0, stage(t + 1), 0, 0);
         load_b<S>(b0, stage(t + 1), 0);
       }
@@ -321,30 +325,31 @@ __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typenam
     Vec16<S> ah[S::FM], bh[S::FN], al[S::FM], bl[S::FN];
     load_a<S>(ah, smem, 0, 0);
     load_b<S>(bh, smem, 0);
-    for (; t < total - 3; ++t) {
+    for (; t < total - D; ++t) {
       load_b<S>(bl, stage(t), 1);
       load_a<S>(al, stage(t), 0, 1);
       mma16<S>(ah, bh, 0, acc);
       mma16<S>(ah, bl, 0, acc);
       interleave16<2 * MM, RR, 0>();
-      arrive16<S::PER>();
+      arrive16<(D - 2) * S::PER>();
       Vec16<S> next[S::FN];
       load_a<S>(ah, stage(t + 1), 0, 0);
       load_b<S>(next, stage(t + 1), 0);
-      issue(t + 3);
+      issue(t + D);
       mma16<S>(al, bh, 0, acc);
       interleave16<MM, RR, S::PER>();
 #pragma unroll
       for (int n = 0; n < S::FN; ++n) bh[n] = next[n];
     }
-    for (; t < total; ++t) {
+    for (bool met = false; t < total; ++t) {
       load_b<S>(bl, stage(t), 1);
       load_a<S>(al, stage(t), 0, 1);
       mma16<S>(ah, bh, 0, acc);
       mma16<S>(ah, bl, 0, acc);
       mma16<S>(al, bh, 0, acc);
       if (t + 1 < total) {
-        arrive(t);
+        if (!met) arrive16<0>();
+        met = true;
         load_a<S>(ah, stage(t + 1), 0, 0);
         load_b<S>(bh, stage(t + 1), 0);
       }

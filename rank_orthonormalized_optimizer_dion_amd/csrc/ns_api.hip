@@ -88,8 +88,16 @@ bool ns_small(int p, int q, int& spp, int& sqp) {
 template <class Pick, class Fill, class Go>
 hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, Pick pick, Fill fill, Go go) {
   NsLaunch L = base;
-  L.nclass = 0;
-  L.total = 0;
+  auto empty = [&] {
+    L.nclass = 0;
+    L.total = 0;
+    for (NsClass& c : L.cls) {
+      c = NsClass{};
+      c.base = INT32_MAX;   // no item is past it
+      c.tiles = 1;
+    }
+  };
+  empty();
   for (const NsClass& s : p.shapes) {
     if (!pick(s)) continue;
     NsClass c = s;
@@ -100,8 +108,7 @@ hipError_t ns_grouped(const NsPlan& p, const NsLaunch& base, Pick pick, Fill fil
     if (L.nclass == kNsMaxClasses) {
       const hipError_t e = go(L);
       if (e != hipSuccess) return e;
-      L.nclass = 0;
-      L.total = 0;
+      empty();
     }
   }
   return L.nclass > 0 ? go(L) : hipSuccess;
@@ -187,9 +194,9 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
     d.q = static_cast<int32_t>(std::max(a.m, a.n));
     d.slot = order[g];
     d.scale = a.scale;
-    // partial sums of at least 8192 elements, at most kNsParts of them
+    // partial sums of at least 2048 elements, at most kNsParts of them
     const int64_t total = a.m * a.n;
-    d.chunk = std::max<int64_t>(8192, ns_cdiv(ns_cdiv(total, kNsParts), 1024) * 1024);
+    d.chunk = std::max<int64_t>(2048, ns_cdiv(ns_cdiv(total, kNsParts), 1024) * 1024);
     d.parts = static_cast<int32_t>(ns_cdiv(total, d.chunk));
     int spp, sqp;
     const bool small = ns_small(d.p, d.q, spp, sqp);

@@ -5,16 +5,38 @@
 
 namespace dion {
 
-// The matrix and the local work item of item t.
+__device__ __forceinline__ int uniform_index(int i) { return __builtin_amdgcn_readfirstlane(i); }
+
+// The matrix and the local work item of item t.  Launch arguments and the
+// table are read through the scalar cache, and every read here that misses
+// it costs about a microsecond before the first tile can be asked for: the
+// classes are all loaded at once and chosen among in registers (unused ones
+// start past every item), and the descriptor is one block of scalar loads.
 __device__ __forceinline__ void ns_locate(const NsLaunch& L, int t, NsDesc& d, NsClass& c, int& local) {
   c = L.cls[0];
 #pragma unroll
-  for (int i = 1; i < kNsMaxClasses; ++i)
-    if (i < L.nclass && t >= L.cls[i].base) c = L.cls[i];
+  for (int i = 1; i < kNsMaxClasses; ++i) {
+    const NsClass k = L.cls[i];
+    const bool in = t >= k.base;
+    c.first = in ? k.first : c.first;
+    c.tiles = in ? k.tiles : c.tiles;
+    c.base = in ? k.base : c.base;
+    c.tx = in ? k.tx : c.tx;
+    c.ty = in ? k.ty : c.ty;
+  }
   const int rel = t - c.base;
   const int mi = rel / c.tiles;
   local = rel - mi * c.tiles;
-  d = L.table ? L.table[c.first + mi] : L.inl;
+  if (L.table) {
+    typedef __attribute__((address_space(4))) const uint32_t* cptr;   // constant memory: scalar loads
+    const cptr src = (cptr)(reinterpret_cast<const uint32_t*>(L.table + uniform_index(c.first + mi)));
+    struct { uint32_t w[sizeof(NsDesc) / 4]; } u;
+#pragma unroll
+    for (size_t i = 0; i < sizeof(NsDesc) / 4; ++i) u.w[i] = src[i];
+    d = __builtin_bit_cast(NsDesc, u);
+  } else {
+    d = L.inl;
+  }
 }
 
 template <typename GT>
