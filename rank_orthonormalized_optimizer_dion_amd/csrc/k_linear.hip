@@ -156,8 +156,8 @@ template <int TILE, int ST, LinKind KIND, int ACT>
 __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
   using S = LinShape<TILE, ST, KIND>;
   __shared__ u32x4 smem[S::LDS_CELLS];
-  const Work16 work{p.full, p.slices, p.part, p.count};
-  const Item16 it = item16(work, xcd_remap(blockIdx.x, gridDim.x));
+  const Work16 work{p.full, p.tx * p.ty - p.full, p.slices, p.part, p.count};
+  const Item16 it = item16(work, xcd_item(blockIdx.x, gridDim.x));
   int ti, tj;
   tile_order(it.tile, p.tx, p.ty, ti, tj);
   const int r0 = ti * TILE, c0 = tj * TILE;

@@ -218,8 +218,8 @@ __global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
   NsDesc d;
   NsClass c;
   int local;
-  const Work16 work{L.full, L.slices, L.part, L.count};
-  const Item16 it = item16(work, xcd_remap(blockIdx.x, gridDim.x));
+  const Work16 work{L.full, L.total - L.full, L.slices, L.part, L.count};
+  const Item16 it = item16(work, xcd_item(blockIdx.x, gridDim.x));
   ns_locate(L, it.tile, d, c, local);
   int ti, tj;
   if constexpr (SYM) {

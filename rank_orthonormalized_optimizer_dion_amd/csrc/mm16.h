@@ -396,12 +396,25 @@ __device__ __forceinline__ void tile_product(const typename S::A& ta, const type
   }
 }
 
+// xcd_remap's chunks for the whole rounds of a launch; its last, partial round
+// (all of a small launch) in one run of consecutive items per XCD, so that
+// the tiles of one matrix meet in one or two L2s there too.
+__device__ __forceinline__ int xcd_item(int b, int nb) {
+  constexpr int ROUND = 8 * kXcdChunk;
+  const int whole = nb / ROUND * ROUND;
+  if (b < whole) return xcd_remap(b, nb);
+  const int rest = nb - whole, x = (b - whole) & 7, each = rest >> 3, more = rest & 7;
+  return whole + x * each + min(x, more) + ((b - whole) >> 3);
+}
+
 // How a launch's tiles share the chip.  Tiles 0 .. full - 1 are one
 // workgroup's each.  The rest, less than a round of the chip's workgroup
 // slots, would leave most of it idle for a whole tile's time: each of them is
 // cut along the reduction into `slices` workgroups.
+// Items go slice by slice: neighbours are then tiles that share panels of the
+// same piece of the reduction.
 struct Work16 {
-  int32_t full, slices;
+  int32_t full, cut, slices;
   float* part;       // a tile of float32 per slice of the cut tiles
   uint32_t* count;   // one per cut tile, zero between launches
 };
@@ -410,8 +423,8 @@ struct Item16 {
 };
 __device__ __forceinline__ Item16 item16(const Work16& w, int t) {
   if (t < w.full) return {t, 0, 1, 0};
-  const int u = t - w.full;
-  return {w.full + u / w.slices, u % w.slices, w.slices, u / w.slices};
+  const int u = t - w.full, slice = u / w.cut, cut = u - slice * w.cut;
+  return {w.full + cut, slice, w.slices, cut};
 }
 
 // The slice of [0, K) that an item works on, in whole stages.
@@ -436,19 +449,24 @@ template <class S>
 __device__ __forceinline__ bool join16(const Work16& w, const Item16& it, u32x4* smem,
                                        typename S::Acc (&acc)[S::FM][S::FN]) {
   if (it.slices == 1) return true;
-  constexpr int Q = sizeof(typename S::Acc) / 8, CELLS = S::BM * S::BN / 2;
-  uint64_t* tile = reinterpret_cast<uint64_t*>(w.part) + static_cast<int64_t>(it.cut) * it.slices * CELLS + threadIdx.x;
-  uint64_t* mine = tile + it.slice * CELLS;
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int Q = sizeof(typename S::Acc) / 16, V = S::FM * S::FN * Q;   // 16-byte pieces per thread
+  constexpr int TILE = S::BM * S::BN * 4;
+  constexpr int DEVICE = 0x10;   // cache policy: device scope
+  constexpr int G = 8;           // pieces of a group: what is in flight has to leave registers to the sums
+  static_assert(V % G == 0, "pieces come in groups");
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      uniform_at(reinterpret_cast<char*>(w.part) + static_cast<int64_t>(it.cut) * it.slices * TILE), 0,
+      it.slices * TILE, 0x00020000);
+  const int lane = threadIdx.x * 16;
 #pragma unroll
-  for (int m = 0; m < S::FM; ++m)
-#pragma unroll
-    for (int n = 0; n < S::FN; ++n)
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        struct { float a, b; } v = {acc[m][n][2 * q], acc[m][n][2 * q + 1]};
-        __hip_atomic_store(mine + ((m * S::FN + n) * Q + q) * S::NT, __builtin_bit_cast(uint64_t, v),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+  for (int i = 0; i < V; ++i) {
+    const typename S::Acc& a = acc[i / Q / S::FN][i / Q % S::FN];
+    const int q = 4 * (i % Q);
+    const f32x4 v = {a[q], a[q + 1], a[q + 2], a[q + 3]};
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, lane + i * (S::NT * 16),
+                                           it.slice * TILE, DEVICE);
+  }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's sums have arrived
   __syncthreads();
@@ -464,21 +482,31 @@ __device__ __forceinline__ bool join16(const Work16& w, const Item16& it, u32x4*
   for (int m = 0; m < S::FM; ++m)
 #pragma unroll
     for (int n = 0; n < S::FN; ++n) acc[m][n] = typename S::Acc{};
-  for (int s = 0; s < it.slices; ++s) {
-    const uint64_t* src = tile + s * CELLS;
+  // two slices' pieces are loaded before the first is added
 #pragma unroll
-    for (int m = 0; m < S::FM; ++m)
+  for (int g = 0; g < V; g += G)
+#pragma unroll 1
+    for (int s = 0; s < it.slices; s += 2) {
+      f32x4 v[2][G];
 #pragma unroll
-      for (int n = 0; n < S::FN; ++n)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          struct F2 { float a, b; };
-          const F2 v = __builtin_bit_cast(F2, __hip_atomic_load(src + ((m * S::FN + n) * Q + q) * S::NT,
-                                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-          acc[m][n][2 * q] += v.a;
-          acc[m][n][2 * q + 1] += v.b;
+        for (int i = 0; i < G; ++i) {
+          v[k][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if (s + k < it.slices)
+            v[k][i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                    rsrc, lane + (g + i) * (S::NT * 16), (s + k) * TILE, DEVICE));
         }
-  }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          typename S::Acc& a = acc[(g + i) / Q / S::FN][(g + i) / Q % S::FN];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[4 * ((g + i) % Q) + e] += v[k][i][e];
+        }
+    }
+#endif
   return true;
 }
 
