@@ -108,72 +108,74 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
   ns_locate(L.common, blockIdx.x, d, c, local);
   const int wave = wave16();
   const int p = uniform32(d.p), q = uniform32(d.q), tall = uniform32(d.tall);
-  const int cols = tall ? p : q;   // as the caller stores it
 
-  // D, in groups of 4 consecutive elements of the caller's rows (of p q
-  // elements, rows of `cols`): every load is in flight before the first use
+  // D, in groups of 4 consecutive columns of X (row i, columns j .. j + 3): a
+  // 16-byte piece of the caller's row when wide; 4 rows of the caller's when
+  // tall, neighbouring lanes then reading neighbouring columns.  Every load
+  // is in flight before the first use.
   constexpr int NG = PP * QP / 4 / (64 * kWaves);
-  const int total = p * q;
-  const bool quads = cols % 4 == 0;
-  const bool vec = quads && d.ldg % 4 == 0 && (reinterpret_cast<uint64_t>(d.G) & (4 * sizeof(GT) - 1)) == 0 &&
+  const bool vec = !tall && q % 4 == 0 && d.ldg % 4 == 0 &&
+                   (reinterpret_cast<uint64_t>(d.G) & (4 * sizeof(GT) - 1)) == 0 &&
                    (reinterpret_cast<uint64_t>(d.M) & 15) == 0;
-  float x[NG][4];
+  const int64_t gi = tall ? 1 : d.ldg, gj = tall ? d.ldg : 1;   // strides of G by X's row and column
+  const int mi = tall ? 1 : q, mj = tall ? p : 1;               // and of M
+  auto group = [&](int u, int& i, int& j) {
+    const int g = threadIdx.x + 64 * kWaves * u;
+    if (tall) {
+      i = g % PP;
+      j = 4 * (g / PP);
+    } else {
+      i = g / (QP / 4);
+      j = 4 * (g % (QP / 4));
+    }
+    return i < p && j < q;
+  };
+  float x[NG][4], m1[NG][4];
   double sum = 0.0;
-  auto each = [&](int u, auto&& f) {   // f(k, row, column, element) of group u
-    const int e = 4 * (threadIdx.x + 64 * kWaves * u);
-    int r = e / cols, col = e - r * cols;
+#pragma unroll
+  for (int u = 0; u < NG; ++u) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[u][k] = m1[u][k] = 0.0f;
+    int i, j;
+    if (!group(u, i, j)) continue;
+    const int64_t o = i * gi + j * gj;
+    const float* mp = d.M + (i * mi + j * mj);
+    if (vec) {
+      if constexpr (sizeof(GT) == 2) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(d.G) + o);
+        x[u][0] = __uint_as_float(w.x << 16);
+        x[u][1] = __uint_as_float(w.x & 0xffff0000u);
+        x[u][2] = __uint_as_float(w.y << 16);
+        x[u][3] = __uint_as_float(w.y & 0xffff0000u);
+      } else {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(d.G) + o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[u][k] = w[k];
+      }
+      if (d.M) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(mp);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m1[u][k] = w[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < q) {
+          x[u][k] = load_g<GT>(d.G, o + k * gj);
+          if (d.M) m1[u][k] = mp[k * mj];
+        }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < NG; ++u)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (e + k < total) f(k, r, col, e + k);
-      if (++col == cols) {
-        col = 0;
-        ++r;
+      if (d.M) {
+        m1[u][k] = ns_moment(L.common, x[u][k], m1[u][k]);
+        x[u][k] = ns_dir(L.common, x[u][k], m1[u][k]);
       }
+      sum += static_cast<double>(x[u][k]) * x[u][k];
     }
-  };
-  {
-    float mom[NG][4];
-#pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      const int e = 4 * (threadIdx.x + 64 * kWaves * u);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[u][k] = mom[u][k] = 0.0f;
-      if (vec) {
-        if (e < total) {
-          const int r = e / cols, col = e - r * cols;
-          const int64_t o = r * d.ldg + col;
-          if constexpr (sizeof(GT) == 2) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(d.G) + o);
-            x[u][0] = __uint_as_float(w.x << 16);
-            x[u][1] = __uint_as_float(w.x & 0xffff0000u);
-            x[u][2] = __uint_as_float(w.y << 16);
-            x[u][3] = __uint_as_float(w.y & 0xffff0000u);
-          } else {
-            const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(d.G) + o);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[u][k] = w[k];
-          }
-          if (d.M) {
-            const f32x4 w = *reinterpret_cast<const f32x4*>(d.M + e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mom[u][k] = w[k];
-          }
-        }
-      } else {
-        each(u, [&](int k, int r, int col, int at) {
-          x[u][k] = load_g<GT>(d.G, r * d.ldg + col);
-          if (d.M) mom[u][k] = d.M[at];
-        });
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < NG; ++u)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (d.M) x[u][k] = ns_dir(L.common, x[u][k], ns_moment(L.common, x[u][k], mom[u][k]));
-        sum += static_cast<double>(x[u][k]) * x[u][k];
-      }
-  }
   sum = wave_sum(sum);
   double* part = reinterpret_cast<double*>(ab);
   if ((threadIdx.x & 63) == 0) part[wave] = sum;
@@ -194,41 +196,37 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < NG; ++u) {
-    const int e = 4 * (threadIdx.x + 64 * kWaves * u);
-    uint16_t hi[4], lo[4];
+    int i, j;
+    if (!group(u, i, j)) continue;
+    // the step's momentum, now that D is known to be finite
+    if (d.M) {
+      float* mp = d.M + (i * mi + j * mj);
+      if (vec) {
+        *reinterpret_cast<f32x4*>(mp) = f32x4{m1[u][0], m1[u][1], m1[u][2], m1[u][3]};
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (j + k < q) mp[k * mj] = m1[u][k];
+      }
+    }
+    uint16_t hi[4], lo[4];   // the columns past q are zero
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float v = pinned(ldexpf(x[u][k], -e2) * L.common.x0);
       hi[k] = to_f16(v);
       lo[k] = to_f16(v - f16_to_f32(hi[k]));
     }
-    if (quads && !tall) {
-      if (e < total) {
-        const int r = e / cols, col = e - r * cols;
-        const int at = 2 * x_cell<QP>(r, col >> 3) + ((col >> 2) & 1);
-        reinterpret_cast<u32x2*>(xh)[at] = u32x2{hi[0] | (static_cast<uint32_t>(hi[1]) << 16), hi[2] | (static_cast<uint32_t>(hi[3]) << 16)};
-        reinterpret_cast<u32x2*>(xl)[at] = u32x2{lo[0] | (static_cast<uint32_t>(lo[1]) << 16), lo[2] | (static_cast<uint32_t>(lo[3]) << 16)};
-      }
-    } else {
-      each(u, [&](int k, int r, int col, int) {
-        const int i = tall ? col : r, j = tall ? r : col;
-        const int at = 8 * x_cell<QP>(i, j >> 3) + (j & 7);
-        reinterpret_cast<uint16_t*>(xh)[at] = hi[k];
-        reinterpret_cast<uint16_t*>(xl)[at] = lo[k];
-      });
-    }
+    const int at = 2 * x_cell<QP>(i, j >> 3) + ((j >> 2) & 1);
+    reinterpret_cast<u32x2*>(xh)[at] = u32x2{hi[0] | (static_cast<uint32_t>(hi[1]) << 16), hi[2] | (static_cast<uint32_t>(hi[3]) << 16)};
+    reinterpret_cast<u32x2*>(xl)[at] = u32x2{lo[0] | (static_cast<uint32_t>(lo[1]) << 16), lo[2] | (static_cast<uint32_t>(lo[3]) << 16)};
   }
-  // the step's momentum, now that D is known to be finite
-  if (d.M)
-    for (int e = threadIdx.x; e < total; e += 64 * kWaves) {
-      const int r = e / cols, col = e - r * cols;
-      d.M[e] = ns_moment(L.common, load_g<GT>(d.G, r * d.ldg + col), d.M[e]);
-    }
   __syncthreads();
 
   const int r0 = 16 * FM * (wave >> 1), c0 = 16 * FN * (wave & 1);   // this wavefront's block of A
   const int col0 = 16 * FC * wave;                                    // and its columns of X
   const int qsteps = (q + 31) / 32;
+  f32x4 y[FC][T::NB];   // (B X)^T on those columns
+  float fy = 0.0f;
   for (int it = 0; it < L.steps; ++it) {
     // a lane number that is new in every iteration: the hundreds of LDS and
     // output addresses made from it would otherwise be computed once, before
@@ -349,7 +347,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
         yh[ks][n] = T::x_col(xh, col0 + 16 * n, ks, lane);
         yl[ks][n] = T::x_col(xl, col0 + 16 * n, ks, lane);
       }
-    f32x4 y[FC][T::NB];
 #pragma unroll
     for (int n = 0; n < FC; ++n)
 #pragma unroll
@@ -379,7 +376,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
         for (int n = 0; n < FC; ++n) y[n][m] = F16::mfma(yh[ks][n], b, y[n][m]);
         if (ks == KS - 1) __builtin_amdgcn_sched_barrier(0);
       }
-    const float fy = s.f_apply * t1;
+    fy = s.f_apply * t1;
     if (!last) {
 #pragma unroll
       for (int n = 0; n < FC; ++n)
@@ -398,26 +395,70 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
           reinterpret_cast<u32x2*>(xl)[at] = u32x2{lo[0] | (static_cast<uint32_t>(lo[1]) << 16), lo[2] | (static_cast<uint32_t>(lo[3]) << 16)};
         }
       __syncthreads();
+    }
+  }
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  // the old weights of a step are loaded before the first new one is
+  // stored: a load cannot be moved over a store that may alias it
+  const int es = L.common.odtype ? 2 : 4;
+  const bool ovec = !tall && d.ldo % 4 == 0 && (reinterpret_cast<uint64_t>(d.O) & (4 * es - 1)) == 0;
+  const int64_t oi = tall ? 1 : d.ldo, oj = tall ? d.ldo : 1;
+  float* w32 = static_cast<float*>(d.O);
+  uint16_t* w16 = static_cast<uint16_t*>(d.O);
+#pragma unroll
+  for (int n = 0; n < FC; ++n) {
+    const int j = col0 + 16 * n + 4 * (lane >> 4);
+    if (j >= q) continue;
+    const bool four = ovec && j + 4 <= q;
+    if (L.step) {
+      float w[T::NB][4];
+#pragma unroll
+      for (int m = 0; m < T::NB; ++m) {
+        const int i = 16 * m + (lane & 15);
+        if (i >= p) continue;
+        if (four) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(w32 + i * oi + j);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[m][k] = v[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[m][k] = j + k < q ? w32[i * oi + (j + k) * oj] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < T::NB; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          y[n][m][k] = fmaf(-d.scale, fy * y[n][m][k], L.common.decay * w[m][k]);
     } else {
 #pragma unroll
-      for (int n = 0; n < FC; ++n)
+      for (int m = 0; m < T::NB; ++m)
 #pragma unroll
-        for (int m = 0; m < T::NB; ++m)
+        for (int k = 0; k < 4; ++k) y[n][m][k] = fy * y[n][m][k];
+    }
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int i = 16 * m + (lane & 15), j = col0 + 16 * n + 4 * (lane >> 4) + v;
-            if (i >= p || j >= q) continue;
-            const int64_t o = tall ? j * d.ldo + i : i * d.ldo + j;
-            const float x = fy * y[n][m][v];
-            if (L.step) {
-              float* w = static_cast<float*>(d.O) + o;
-              *w = fmaf(-d.scale, x, L.common.decay * *w);
-            } else if (L.common.odtype) {
-              static_cast<uint16_t*>(d.O)[o] = to_bf16(x);
-            } else {
-              static_cast<float*>(d.O)[o] = x;
-            }
-          }
+    for (int m = 0; m < T::NB; ++m) {
+      const int i = 16 * m + (lane & 15);
+      if (i >= p) continue;
+      const f32x4 v = y[n][m];
+      const int64_t o = i * oi + j * oj;
+      if (L.common.odtype) {
+        const uint16_t h[4] = {to_bf16(v[0]), to_bf16(v[1]), to_bf16(v[2]), to_bf16(v[3])};
+        if (four) {
+          *reinterpret_cast<u32x2*>(w16 + o) = u32x2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (j + k < q) w16[o + k * oj] = h[k];
+        }
+      } else if (four) {
+        *reinterpret_cast<f32x4*>(w32 + o) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (j + k < q) w32[o + k * oj] = v[k];
+      }
     }
   }
 }
