@@ -74,10 +74,15 @@ int ns_validate(const NsMatrix& a, int gdtype, int odtype, bool step) {
   return DION_OK;
 }
 
-// Whether a p x q matrix (p <= q) takes the one-workgroup form, and the
-// padded sides it takes it with: X's planes and one p x p plane have to fit
-// 160 KB of LDS.
+// Whether a p x q matrix (p <= q) takes a one-workgroup form, and the padded
+// sides it takes it with: plain float32 for at most 16 rows (sqp = 0), else
+// the matrix cores, where X's planes and one p x p plane fit 160 KB of LDS.
 bool ns_small(int p, int q, int& spp, int& sqp) {
+  if (p <= kNsTinySide && static_cast<int64_t>(p) * q <= kNsTinyFloats) {
+    spp = p <= 1 ? 1 : p <= 2 ? 2 : p <= 4 ? 4 : p <= 8 ? 8 : 16;
+    sqp = 0;
+    return true;
+  }
   spp = p <= 64 ? 64 : 128;
   sqp = q <= 128 ? 128 : q <= 256 ? 256 : 512;
   return p <= 128 && q <= (p <= 64 ? 512 : 256);
@@ -281,6 +286,9 @@ NsSmall ns_small_args(const NsLaunch& L, const std::vector<NsIter>& it, bool ste
     a.it[k] = {static_cast<float>(s.sa / (s.sx * s.sx)), static_cast<float>(s.c * s.sb / (s.sa * s.sa)),
                static_cast<float>(s.b * s.sb / s.sa), static_cast<float>(s.a * s.sb),
                static_cast<float>(next / (s.sb * s.sx))};
+    a.coef[k][0] = static_cast<float>(s.a);
+    a.coef[k][1] = static_cast<float>(s.b);
+    a.coef[k][2] = static_cast<float>(s.c);
   }
   return a;
 }
@@ -307,11 +315,16 @@ hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool
     }
     L.table = dst;
   }
-  for (int v = 0; v < 5; ++v) {   // the one-workgroup forms
-    const int spp = v < 3 ? 64 : 128, sqp = v < 3 ? 128 << v : 128 << (v - 3);
+  constexpr int kForms[][2] = {{64, 128}, {64, 256}, {64, 512}, {128, 128}, {128, 256},
+                               {1, 0}, {2, 0}, {4, 0}, {8, 0}, {16, 0}};
+  for (const auto& form : kForms) {   // the one-workgroup forms
+    const int spp = form[0], sqp = form[1];
     NS_TRY(ns_grouped(p, L, [=](const NsClass& c) { return c.planes == 0 && c.spp == spp && c.sqp == sqp; },
                       [](const NsDesc&, NsClass& c) { c.tiles = 1; },
-                      [&](const NsLaunch& K) { return launch_ns_small(ns_small_args(K, it, step), spp, sqp, st); }));
+                      [&](const NsLaunch& K) {
+                        const NsSmall a = ns_small_args(K, it, step);
+                        return sqp == 0 ? launch_ns_tiny(a, spp, st) : launch_ns_small(a, spp, sqp, st);
+                      }));
   }
   NS_TRY(ns_grouped(p, L, [](const NsClass& c) { return c.planes != 0; },
                     [](const NsDesc& d, NsClass& c) { c.tiles = d.parts; },

@@ -46,7 +46,7 @@ struct NsDesc {
 
 struct NsClass {
   int32_t planes;         // 0: the one-workgroup form
-  int32_t spp, sqp;       // its padded sides
+  int32_t spp, sqp;       // its padded sides; sqp = 0: k_ns_tiny with spp >= p rows
   int32_t first, count;   // matrices of this shape in the table
   int32_t tiles, base;    // work items per matrix, first item
   int32_t tx, ty;         // tile grid
@@ -91,7 +91,11 @@ struct NsSmall {
   NsLaunch common;        // classes (tiles = 1), status, momentum, types
   int32_t steps, step;    // step: Muon step, else the output is written
   Iter it[kNsMaxSteps];
+  float coef[kNsMaxSteps][3];   // a, b, c (k_ns_tiny)
 };
+// k_ns_tiny: p <= 16 and p q <= kNsTinyFloats, X in LDS as float32
+constexpr int kNsTinySide = 16;
+constexpr int kNsTinyFloats = 32768;
 
 struct NsUpload {
   NsDesc d[kNsUpload];
@@ -102,6 +106,8 @@ struct NsUpload {
 hipError_t launch_ns_table(const NsUpload& u, hipStream_t st);
 // pp, qp: (64, 128), (64, 256), (64, 512), (128, 128) or (128, 256)
 hipError_t launch_ns_small(const NsSmall& L, int pp, int qp, hipStream_t st);
+// p: 1, 2, 4, 8 or 16
+hipError_t launch_ns_tiny(const NsSmall& L, int p, hipStream_t st);
 hipError_t launch_ns_norm(const NsLaunch& L, hipStream_t st);
 hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st);
 // tile: 128 or 256

@@ -322,3 +322,25 @@ def test_large_reductions_are_cut(gpu_lib):
         gpu_lib.orthogonalize(G, P, math=mode)
         assert rel(O, ns64(G.double(), [Q] * 5)) <= tol
         assert torch.equal(O, P)
+
+
+@pytest.mark.parametrize("m,n", [(1, 32768), (1, 32769), (16, 2048), (16, 2049), (2048, 16), (3, 6000), (9, 9), (16, 16),
+                                 (17, 17), (8, 1000), (1000, 2)])
+def test_few_rows(gpu_lib, m, n):
+    """Matrices of few singular values, whose roundings do not average: the
+    float32 form (up to 16 rows that fit the LDS) and its neighbours."""
+    import torch
+    say(f"ns few rows {m}x{n}")
+    for dt in (torch.float32, torch.bfloat16):
+        G = draw(m, n, 400 + m + n, dt)
+        O = torch.full((m, n), float("nan"), device="cuda")
+        for cs in ([Q] * 5, [CUBIC] * 4):
+            ws = gpu_lib.orthogonalize(G, O, cs, len(cs), "f32")
+            gpu_lib.check_status(ws, 1)
+            assert rel(O, ns64(G.double(), cs)) <= TOL32
+    X, M = draw(m, n, 1, torch.float32) * 0.02, draw(m, n, 2, torch.float32)
+    x, mm = muon64(X.double(), G.double(), M.double(), 0.02, 0.95, False, 0.1, 1.0, [Q] * 5)
+    gpu_lib.muon_step(X, G, M, 0.02, 0.95, False, 0.1, "none", Q, 5)
+    assert rel(M, mm) <= 2.0 ** -22
+    bound = TOL32 * 0.02 * min(m, n) ** 0.5 * 1.2 + 2.0 ** -22 * float(torch.linalg.vector_norm(x))
+    assert float(torch.linalg.vector_norm(X.double() - x)) <= bound
