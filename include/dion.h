@@ -399,8 +399,10 @@ int dion_muon_step(float* X, const void* G, float* M, int64_t m, int64_t n, floa
  * before the two products when there is an activation and more than 64
  * tokens.  float32 products are
  * taken as six bfloat16 products of three-way split operands (24 bits, errors
- * of float32's order); a non-finite operand makes the outputs it reaches
- * non-finite, not always with the sign float32 would give.
+ * of float32's order; with more than 8 tokens, and in the backward pass, a
+ * value below 2^-110 is taken to within 2^-134); a non-finite operand makes
+ * the outputs it reaches non-finite, not always with the sign float32 would
+ * give.
  *
  * Forward reads x, w, bias (or NULL), residual (or NULL; y itself is allowed)
  * and writes y and, when z is not NULL, z.  Backward reads dy, z (only with

@@ -10,7 +10,8 @@
 // transposed on their way out of LDS (mm16.h), so no transposed copy of an
 // activation or a weight is ever written.  float32 tensors are first split
 // three ways into bfloat16 planes (24 bits) and multiplied as six plane
-// products, float32's accuracy over float32's range.
+// products: float32's accuracy for values from 2^-110 up to the largest
+// (below, the planes end at 2^-133).
 //
 // Bound and measured (MI355X): large batches by the matrix cores (8192
 // tokens, 8192 -> 3072 with GELU, bias and residual: 438 us, 0.94 PFLOP/s; the
@@ -198,6 +199,16 @@ __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
       });
 }
 
+// The first of several planes of x.  A finite x above bfloat16's largest
+// number would round to infinity and leave -infinity for the next plane; it
+// is cut off instead (float32's largest and bfloat16's share the exponent),
+// which leaves a remainder of 16 bits that two planes hold exactly.
+__device__ __forceinline__ uint16_t first_plane(float x) {
+  const uint16_t h = to_bf16(x);
+  const uint32_t b = __float_as_uint(x);
+  return (h & 0x7fff) == 0x7f80 && (b & 0x7fffffffu) < 0x7f800000u ? static_cast<uint16_t>(b >> 16) : h;
+}
+
 // dz = src act'(z) (or src itself) as planes, zero past its columns and rows,
 // and its column sums over this workgroup's `chunk` rows.  256 columns by 8
 // row lanes per workgroup.
@@ -231,7 +242,7 @@ __device__ __forceinline__ void pack_block(const LinPack& p, int block, float (&
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float x = pinned(pl == 0 ? v[k] : rest[k]);
-            h[k] = to_bf16(x);
+            h[k] = pl == 0 && p.planes > 1 ? first_plane(x) : to_bf16(x);
             rest[k] = x - bf16_to_f32(h[k]);
           }
           *reinterpret_cast<u32x4*>(at + pl * p.plane) = pack8(h);

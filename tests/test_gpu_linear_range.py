@@ -62,3 +62,59 @@ def test_gelu_slope_element_by_element(gpu_lib, t, dtype):
     rest = z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
     slack = (gelu_bound(z) + U32) * (phi + rest.abs())
     assert torch.all((dx.double() - (phi + rest)).abs() <= out * (phi + rest).abs() + slack)
+
+
+#: float32 numbers at the top of the range: from FLT_MAX down across the
+#: midpoint (about 3.396e38) from which rounding to bfloat16 gives infinity.
+TOP = (3.4028234663852886e38, -3.4e38, 3.3962e38, -3.39615e38, 3.39e38, 1e38, -2e37, 1.0)
+
+
+@pytest.mark.parametrize("t", [4, 40, 130])
+def test_float32_values_near_the_largest(gpu_lib, t):
+    """x (forward) and dy (backward) with entries up to FLT_MAX against small
+    weights: every output is finite in float32 and has float32's accuracy."""
+    import torch
+    say(f"linear top {t}")
+    g = torch.Generator(device="cuda").manual_seed(t)
+    big = torch.tensor(TOP, device="cuda").repeat(t * 8).view(t, 64)
+    w = torch.randn(64, 64, generator=g, device="cuda") * 1e-3
+    y = torch.empty_like(big)
+    gpu_lib.linear_forward(big, w, y)
+    assert rel(y, big.double() @ w.double().T) <= 2.0 ** -19
+    x = torch.randn(t, 64, generator=g, device="cuda") * 1e-4
+    dx, dw = torch.empty_like(big), torch.empty_like(w)
+    gpu_lib.linear_backward(big, x, w, dx=dx, dw=dw)
+    assert rel(dx, big.double() @ w.double()) <= 2.0 ** -19
+    assert rel(dw, big.double().T @ x.double()) <= 2.0 ** -19
+
+
+def test_few_tokens_gradient_near_the_largest(gpu_lib):
+    """bfloat16, at most 64 tokens, an activation: dz = dy act'(z) is held in
+    two planes and may lie above the largest bfloat16 number in float32."""
+    import torch
+    t = 40
+    z = torch.linspace(1.2, 1.3, t * 64, device="cuda").view(t, 64).bfloat16()
+    zz = z.double()
+    s = torch.sigmoid(zz)
+    slope = s * (1 + zz * (1 - s))
+    dy = torch.full_like(z, 3.3895313892515355e38)     # the largest
+    dz = dy.double() * slope
+    over = (dz > 3.3962e38) & (dz < 3.4028e38)
+    assert over.any()
+    dy = torch.where(over, dy, torch.zeros_like(dy))
+    dz = dy.double() * slope
+    w, dx = (torch.eye(64, device="cuda") * 2.0 ** -10).bfloat16(), torch.empty_like(z)
+    gpu_lib.linear_backward(dy, weight=w, dx=dx, act="silu", preact=z)
+    assert rel(dx, dz * 2.0 ** -10) <= 2.0 ** -8 + 2.0 ** -16
+
+
+@pytest.mark.parametrize("t", [4, 40, 130])
+def test_float32_values_near_zero(gpu_lib, t):
+    """Entries below 2^-110: the planes end at 2^-133, so an entry is taken to
+    within half of that (and the products with 1 are exact)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(t, 64, generator=g, device="cuda") * 2.0 ** -118
+    w, y = torch.eye(64, device="cuda"), torch.empty_like(x)
+    gpu_lib.linear_forward(x, w, y)
+    assert float((y.double() - x.double()).abs().max()) <= 2.0 ** -134
