@@ -9,9 +9,14 @@ when the built library is missing.
     import rank_orthonormalized_optimizer_dion_amd as dion
     ws = dion.step(X, G, R, V, eta=0.01, beta=0.95, variant="orth")
     dion.check_status(ws, 1)        # optional: waits, raises on breakdown
+
+Work is enqueued on ``stream`` (a torch stream; default: the current one) and
+is ordered behind that stream's earlier work only: tensors that another stream
+writes have to be waited for there (``stream.wait_stream``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -229,6 +234,15 @@ def workspace_size(m: int, n: int, r: int, variant="orth", g_dtype=None, math="f
     if size == 0:
         raise ValueError("invalid shape or rank")
     return int(size)
+
+
+def _new_workspace(nbytes: int, device, stream):
+    """nbytes from the memory of the stream that will use them: memory of
+    another stream's pool may be in use by work that is still pending there,
+    and nothing would order that before this use."""
+    torch = _torch()
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _workspace(nbytes: int, device, workspace):
@@ -492,17 +506,13 @@ def _check_rows(name, t, shape=None, dtypes=None, device=None):
 
 def _launch(size, run, device, workspace, stream):
     """run(pointer, bytes, stream) on `device` with the caller's workspace, or
-    with a new one of size() bytes; returns the workspace.  A new one that
-    another stream than the current one uses is marked so for torch's
-    allocator."""
+    with a new one of size() bytes; returns the workspace."""
     torch = _torch()
     if workspace is None:
         nbytes = size()
         if nbytes == 0:
             raise _err(ERR_INVALID_ARG)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _new_workspace(nbytes, device, stream)
     else:
         if workspace.device != device:
             raise ValueError(f"workspace is on {workspace.device}, expected {device}")
