@@ -245,10 +245,9 @@ def _new_workspace(nbytes: int, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _workspace(nbytes: int, device, workspace):
-    torch = _torch()
+def _workspace(nbytes: int, device, workspace, stream=None):
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return _new_workspace(nbytes, device, stream)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace too small: need {nbytes} bytes")
     return workspace
@@ -267,7 +266,7 @@ def step(X, G, R, V, eta: float, beta: float, variant="orth", workspace=None, st
     nbytes = lib.dion_workspace_size(m, n, r, var, gd)
     if nbytes == 0:
         raise _err(ERR_INVALID_ARG)
-    ws = _workspace(nbytes, X.device, workspace)
+    ws = _workspace(nbytes, X.device, workspace, stream)
     rc = lib.dion_step(X.data_ptr(), G.data_ptr(), R.data_ptr(), V.data_ptr(), m, n, r,
                        float(eta), float(beta), var, gd, ws.data_ptr(), nbytes,
                        _stream_handle(stream, X.device))
@@ -328,7 +327,7 @@ def step_batched(mats: Sequence[Tuple], eta: float, beta: float, variant="orth",
     if nbytes == 0:
         raise _err(ERR_INVALID_ARG)
     dev = mats[0][0].device
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _workspace(nbytes, dev, workspace, stream)
     rc = lib.dion_step_batched(arr, len(mats), float(eta), float(beta), var, gd,
                                ws.data_ptr(), nbytes, _stream_handle(stream, dev))
     if rc != OK:
@@ -355,8 +354,10 @@ class Plan:
         self._h = h
         self.workspace_bytes = int(self._lib.dion_plan_workspace_size(h))
 
-    def new_workspace(self):
-        return _workspace(self.workspace_bytes, self.device, None)
+    def new_workspace(self, stream=None):
+        """stream: the one that will run the steps, where it is not the
+        current one."""
+        return _workspace(self.workspace_bytes, self.device, None, stream)
 
     def step(self, eta: float, beta: float, workspace, stream=None):
         if self._h is None:

@@ -84,6 +84,28 @@ def test_training_operators(torch, stream, where):
     assert len(torch.made) == 1
 
 
+@pytest.mark.parametrize("stream,where", [(None, MAIN), (SIDE, SIDE)])
+@pytest.mark.parametrize("call", ["step", "step_batched", "plan"])
+def test_optimizer_step(torch, monkeypatch, call, stream, where):
+    class Lib:
+        dion_workspace_size = dion_workspace_size_batched = dion_plan_workspace_size = \
+            staticmethod(lambda *a: 640)
+        dion_step = dion_step_batched = dion_plan_create = staticmethod(lambda *a: dion.OK)
+        dion_plan_destroy = staticmethod(lambda h: None)
+
+    mat = types.SimpleNamespace(device=DEVICE, data_ptr=lambda: 1 << 20)
+    monkeypatch.setattr(dion, "load", lambda: Lib)
+    monkeypatch.setattr(dion, "_check", lambda X, G, R, V: (8, 8, 4))
+    monkeypatch.setattr(dion, "_gdtype", lambda G: 0)
+    if call == "step":
+        ws = dion.step(mat, mat, mat, mat, 0.1, 0.9, stream=stream)
+    elif call == "step_batched":
+        ws = dion.step_batched([(mat,) * 4], 0.1, 0.9, stream=stream)
+    else:
+        ws = dion.Plan([(mat,) * 4]).new_workspace(stream)
+    assert ws.stream is where and torch.cuda.now is MAIN
+
+
 @pytest.mark.gpu
 def test_on_the_gpu(gpu_lib):
     """The allocator's own record: the block belongs to the call's stream."""
