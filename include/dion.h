@@ -365,7 +365,8 @@ int dion_orthogonalize(const void* G, int64_t ldg, void* O, int64_t ldo,
  *   D  = G + mu M (nesterov != 0) or M
  *   X <- (1 - lr weight_decay) X - lr scale O,   O = orthogonalize(D)
  * X and M are updated in place.  scale is the caller's per-matrix factor
- * (for example sqrt(max(1, m / n))). */
+ * (for example sqrt(max(1, m / n))); lr scale and 1 - lr weight_decay have to be
+ * finite in float32. */
 typedef struct dion_muon_matrix {
   float*      X;        /* m x n, updated in place */
   const void* G;        /* m x n, read only */

@@ -470,7 +470,8 @@ DION_API int dion_muon_step_batched(const dion_muon_matrix* mats, int count, flo
                                     int math, int g_dtype, void* workspace, size_t workspace_bytes,
                                     void* stream) {
   if (!mats || count < 1 || count > DION_MAX_LIST) return DION_ERR_INVALID_ARG;
-  if (!std::isfinite(lr) || !std::isfinite(momentum) || !std::isfinite(weight_decay))
+  const float decay = 1.0f - lr * weight_decay;
+  if (!std::isfinite(lr) || !std::isfinite(momentum) || !std::isfinite(weight_decay) || !std::isfinite(decay))
     return DION_ERR_INVALID_ARG;
   return ns_guard([&] {
     NsLaunch L{};
@@ -478,7 +479,7 @@ DION_API int dion_muon_step_batched(const dion_muon_matrix* mats, int count, flo
     L.odtype = DION_DTYPE_F32;
     L.mu = momentum;
     L.nesterov = nesterov != 0;
-    L.decay = 1.0f - lr * weight_decay;
+    L.decay = decay;
     return ns_run(ns_list(mats, count, lr), L, coeffs, steps, math, true, workspace, workspace_bytes, stream);
   });
 }
