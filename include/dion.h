@@ -334,8 +334,9 @@ int dion_status(const void* workspace, int count, void* stream, int* per_matrix)
  * step, a non-finite momentum) sets DION_STATUS_NONFINITE in its status word
  * (dion_status) and leaves O, or X and M, as they were.  The conventions at
  * the top of this header hold, with these differences: G and O have row
- * pitches ldg, ldo >= n (elements); m, n >= 1 with m n < 2^31 and any order;
- * a list holds at most DION_MAX_LIST matrices.  The list is read before the
+ * pitches ldg, ldo >= n (elements) and may be column blocks of one buffer, of
+ * one pitch; m, n >= 1 with m n < 2^31 and any order; a list holds at most
+ * DION_MAX_LIST matrices.  The list is read before the
  * call returns.  The same call gives the same bits; a matrix's last bits may
  * depend on the other matrices of the list (long sums are cut to fill the
  * chip). */
@@ -409,7 +410,8 @@ int dion_muon_step(float* X, const void* G, float* M, int64_t m, int64_t n, floa
  * and writes y and, when z is not NULL, z.  Backward reads dy, z (only with
  * an activation), x (for dw) and w (for dx) and writes those of dx, dw and db
  * that are not NULL; with accumulate != 0, dw and db are added to.  Outputs
- * overlap nothing else.  Sums are taken in a fixed order: the same call gives
+ * share no element with anything else (column blocks of one buffer, of one
+ * pitch, are apart).  Sums are taken in a fixed order: the same call gives
  * the same bits.  Size queries return 0 for invalid arguments; errors as for
  * the calls above. */
 #define DION_ACT_NONE  0

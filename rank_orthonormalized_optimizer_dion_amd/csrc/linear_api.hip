@@ -8,6 +8,7 @@
 
 #include "dion.h"
 #include "linear_types.h"
+#include "span.h"
 #include "work16.h"
 
 #define DION_API extern "C" __attribute__((visibility("default")))
@@ -27,20 +28,6 @@ constexpr int64_t kLinDirectPitch = int64_t{1} << 22;
 // too few terms there, and the products' time is the weights' traffic.
 constexpr int kLinFewTokens = 64;
 constexpr int64_t kLinBigTiles = 256;   // 256 x 256 tiles in a product of at least this many
-
-struct Span {
-  const void* p;
-  int64_t rows, cols, ld;
-  int64_t esize;
-  bool misplaced() const { return reinterpret_cast<uintptr_t>(p) % esize != 0; }
-  size_t bytes() const { return rows > 0 ? static_cast<size_t>(((rows - 1) * ld + cols) * esize) : 0; }
-};
-
-bool lin_overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.bytes() && y < x + a.bytes();
-}
 
 bool span_ok(const Span& s, bool required) {
   if (!s.p) return !required || s.rows == 0;
@@ -80,10 +67,10 @@ bool lin_forward_ok(const dion_linear* l, LinCall& c) {
       !span_ok(c.z, false) || !span_ok(c.bias, false))
     return false;
   for (const Span* in : {&c.x, &c.w, &c.bias})
-    if (lin_overlap(*in, c.y) || lin_overlap(*in, c.z)) return false;
-  if (lin_overlap(c.y, c.z) || lin_overlap(c.res, c.z)) return false;
+    if (spans_overlap(*in, c.y) || spans_overlap(*in, c.z)) return false;
+  if (spans_overlap(c.y, c.z) || spans_overlap(c.res, c.z)) return false;
   // y may be the residual itself (added in place), not a shifted view of it
-  if (lin_overlap(c.res, c.y) && !(c.res.p == c.y.p && c.res.ld == c.y.ld)) return false;
+  if (spans_overlap(c.res, c.y) && !(c.res.p == c.y.p && c.res.ld == c.y.ld)) return false;
   return true;
 }
 
@@ -95,9 +82,9 @@ bool lin_backward_ok(const dion_linear* l, LinCall& c) {
   const Span* outs[] = {&c.dx, &c.dw, &c.db};
   for (int i = 0; i < 3; ++i) {
     for (const Span* in : {&c.dy, &c.z, &c.x, &c.w})
-      if (lin_overlap(*in, *outs[i])) return false;
+      if (spans_overlap(*in, *outs[i])) return false;
     for (int j = 0; j < i; ++j)
-      if (lin_overlap(*outs[i], *outs[j])) return false;
+      if (spans_overlap(*outs[i], *outs[j])) return false;
   }
   return true;
 }

@@ -9,6 +9,7 @@
 
 #include "dion.h"
 #include "ns_types.h"
+#include "span.h"
 #include "work16.h"
 
 #define DION_API extern "C" __attribute__((visibility("default")))
@@ -50,11 +51,6 @@ bool ns_math(int math, int& planes) {
   return true;
 }
 
-bool ns_overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
 bool ns_shape_ok(const NsMatrix& a) {
   return a.m >= 1 && a.n >= 1 && a.m <= DION_MAX_DIM && a.n <= DION_MAX_DIM && a.m * a.n <= INT32_MAX;
 }
@@ -63,13 +59,11 @@ int ns_validate(const NsMatrix& a, int gdtype, int odtype, bool step) {
   if (!ns_shape_ok(a)) return DION_ERR_INVALID_ARG;
   if (!a.G || !a.O || (step && !a.M)) return DION_ERR_INVALID_ARG;
   if (a.ldg < a.n || a.ldo < a.n || a.ldg > INT32_MAX || a.ldo > INT32_MAX) return DION_ERR_INVALID_ARG;
-  const size_t eg = gdtype == DION_DTYPE_BF16 ? 2 : 4, eo = odtype == DION_DTYPE_BF16 ? 2 : 4;
-  auto off = [](const void* p, size_t al) { return reinterpret_cast<uintptr_t>(p) % al != 0; };
-  if (off(a.G, eg) || off(a.O, eo) || (step && off(a.M, 4))) return DION_ERR_INVALID_ARG;
-  const size_t sg = ((a.m - 1) * a.ldg + a.n) * eg, so = ((a.m - 1) * a.ldo + a.n) * eo;
-  const size_t sm = static_cast<size_t>(a.m) * a.n * 4;
-  if (ns_overlap(a.G, sg, a.O, so)) return DION_ERR_INVALID_ARG;
-  if (step && (ns_overlap(a.G, sg, a.M, sm) || ns_overlap(a.O, so, a.M, sm))) return DION_ERR_INVALID_ARG;
+  const Span g{a.G, a.m, a.n, a.ldg, gdtype == DION_DTYPE_BF16 ? 2 : 4};
+  const Span o{a.O, a.m, a.n, a.ldo, odtype == DION_DTYPE_BF16 ? 2 : 4};
+  const Span m{a.M, a.m, a.n, a.n, 4};   // the step's
+  if (g.misplaced() || o.misplaced() || m.misplaced()) return DION_ERR_INVALID_ARG;
+  if (spans_overlap(g, o) || spans_overlap(g, m) || spans_overlap(o, m)) return DION_ERR_INVALID_ARG;
   if (step && !std::isfinite(a.scale)) return DION_ERR_INVALID_ARG;
   return DION_OK;
 }

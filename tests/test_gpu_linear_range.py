@@ -118,3 +118,37 @@ def test_float32_values_near_zero(gpu_lib, t):
     w, y = torch.eye(64, device="cuda"), torch.empty_like(x)
     gpu_lib.linear_forward(x, w, y)
     assert float((y.double() - x.double()).abs().max()) <= 2.0 ** -134
+
+
+def test_columns_of_one_buffer(gpu_lib):
+    """y, z and the residual beside x in one buffer, dx beside dy: the bits of
+    separate tensors, and the columns between them untouched."""
+    import torch
+    for dtype in (torch.float32, torch.bfloat16):
+        for t in (3, 40, 140):
+            g = torch.Generator(device="cuda").manual_seed(t)
+            buf = torch.randn(t, 200, generator=g, device="cuda").to(dtype)
+            w = (torch.randn(32, 64, generator=g, device="cuda") * 0.1).to(dtype)
+            x, y, z, r = buf[:, :64], buf[:, 64:96], buf[:, 96:128], buf[:, 129:161]
+            x0, r0, gap = x.clone(), r.clone(), (buf[:, 128].clone(), buf[:, 161:].clone())
+            want, zwant = torch.empty(t, 32, dtype=dtype, device="cuda"), torch.empty(t, 32, dtype=dtype, device="cuda")
+            gpu_lib.linear_forward(x0, w, want, act="silu", residual=r0, preact=zwant)
+            gpu_lib.linear_forward(x, w, y, act="silu", residual=r, preact=z)
+            assert torch.equal(y, want) and torch.equal(z, zwant)
+            assert torch.equal(x, x0) and torch.equal(r, r0)
+            assert torch.equal(buf[:, 128], gap[0]) and torch.equal(buf[:, 161:], gap[1])
+            dxw = torch.empty(t, 64, dtype=dtype, device="cuda")
+            gpu_lib.linear_backward(r0, weight=w, dx=dxw)
+            gpu_lib.linear_backward(r, weight=w, dx=x)
+            assert torch.equal(x, dxw) and torch.equal(r, r0) and torch.equal(y, want)
+
+
+def test_orthogonalize_beside_its_input(gpu_lib):
+    import torch
+    for m, n in ((3, 40), (70, 40), (300, 200)):
+        g = torch.Generator(device="cuda").manual_seed(m)
+        buf = torch.randn(m, 2 * n, generator=g, device="cuda")
+        g0, want = buf[:, :n].clone(), torch.empty(m, n, device="cuda")
+        gpu_lib.orthogonalize(g0, want)
+        gpu_lib.orthogonalize(buf[:, :n], buf[:, n:])
+        assert torch.equal(buf[:, n:], want) and torch.equal(buf[:, :n], g0)
