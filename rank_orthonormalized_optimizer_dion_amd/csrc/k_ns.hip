@@ -124,14 +124,7 @@ __global__ __launch_bounds__(256) void k_ns_load(NsLaunch L) {
   NsClass c;
   int local;
   ns_locate(L, blockIdx.x, d, c, local);
-  double sum = 0.0;
-  const double* parts = reinterpret_cast<const double*>(L.ws + d.oS);
-  for (int i = threadIdx.x; i < d.parts; i += 256) sum += parts[i];
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  sum = (part[0] + part[1]) + (part[2] + part[3]);
-  const double norm = sqrt(sum);
+  const double norm = ns_norm<4>(L, d, part);
   const bool finite = norm < 1.7e308;   // false for NaN too
   if (local == 0 && threadIdx.x == 0) {
     if (!finite) L.status[d.slot] = kNsNonFinite;

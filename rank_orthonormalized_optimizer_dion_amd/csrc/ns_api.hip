@@ -69,18 +69,21 @@ int ns_validate(const NsMatrix& a, int gdtype, int odtype, bool step) {
 }
 
 // Whether a p x q matrix (p <= q) takes a one-workgroup form, and the padded
-// sides it takes it with: plain float32 for at most 16 rows (sqp = 0), else
-// the matrix cores, where X's planes and one p x p plane fit 160 KB of LDS.
+// sides it takes it with: plain float32 for at most 16 rows (sqp = 0; those
+// that do not fit take k_ns_rows), else the matrix cores, where X's planes and
+// one p x p plane fit 160 KB of LDS.
 bool ns_small(int p, int q, int& spp, int& sqp) {
-  if (p <= kNsTinySide && static_cast<int64_t>(p) * q <= kNsTinyFloats) {
+  if (p <= kNsTinySide) {
     spp = p <= 1 ? 1 : p <= 2 ? 2 : p <= 4 ? 4 : p <= 8 ? 8 : 16;
     sqp = 0;
-    return true;
+    return static_cast<int64_t>(p) * q <= kNsTinyFloats;
   }
   spp = p <= 64 ? 64 : 128;
   sqp = q <= 128 ? 128 : q <= 256 ? 256 : 512;
   return p <= 128 && q <= (p <= 64 ? 512 : 256);
 }
+
+int ns_row_chunks(int q) { return static_cast<int>(ns_cdiv(q, ns_row_cols(q))); }
 
 // One grouped launch per kNsMaxClasses shapes; the shapes are those that
 // `pick` accepts.
@@ -199,9 +202,15 @@ void ns_layout(const std::vector<NsMatrix>& mats, int planes, NsPlan& p) {
     d.parts = static_cast<int32_t>(ns_cdiv(total, d.chunk));
     int spp, sqp;
     const bool small = ns_small(d.p, d.q, spp, sqp);
-    d.planes = small ? 0 : d.p <= kNsSmallSide ? 2 : planes;
+    d.planes = small ? 0 : d.p <= kNsTinySide ? kNsFewRows : d.p <= kNsSmallSide ? 2 : planes;
     const size_t row = 2 * d.planes * ns_pad(d.p);
-    if (!small) {
+    if (d.planes == kNsFewRows) {
+      const size_t sums = sizeof(float) * ns_row_chunks(d.q) * (spp * (spp + 1) / 2);
+      d.oX = take(sizeof(float) * d.p * ns_row_pitch(d.q));
+      d.oA = take(sums);
+      d.oB = take(sums);
+      d.oS = take(kNsParts * 8);
+    } else if (!small) {
       d.oX = take(2 * row * ns_pitch(d.q, d.planes));
       d.oA = take(row * ns_pitch(d.p, d.planes));
       d.oB = take(row * ns_pitch(d.p, d.planes));
@@ -287,6 +296,22 @@ NsSmall ns_small_args(const NsLaunch& L, const std::vector<NsIter>& it, bool ste
   return a;
 }
 
+// The stages of k_ns_rows, over the matrices of each number of rows.
+hipError_t ns_rows(const NsPlan& p, const NsLaunch& base, const std::vector<NsIter>& it, bool step, hipStream_t st) {
+  const int steps = static_cast<int>(it.size());
+  for (int stage = 0; stage <= steps; ++stage)
+    for (const int rows : {1, 2, 4, 8, 16})
+      NS_TRY(ns_grouped(p, base, [=](const NsClass& c) { return c.planes == kNsFewRows && c.spp == rows; },
+                        [](const NsDesc& d, NsClass& c) { c.tiles = ns_row_chunks(d.q); },
+                        [&](const NsLaunch& K) {
+                          const NsIter s = stage > 0 ? it[stage - 1] : NsIter{};
+                          return launch_ns_rows({K, stage, steps, step, static_cast<float>(s.a),
+                                                 static_cast<float>(s.b), static_cast<float>(s.c)},
+                                                rows, st);
+                        }));
+  return hipSuccess;
+}
+
 hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool step,
                       char* ws, hipStream_t st) {
   L.ws = ws;
@@ -323,6 +348,7 @@ hipError_t ns_enqueue(NsPlan& p, NsLaunch L, const std::vector<NsIter>& it, bool
   NS_TRY(ns_grouped(p, L, [](const NsClass& c) { return c.planes != 0; },
                     [](const NsDesc& d, NsClass& c) { c.tiles = d.parts; },
                     [&](const NsLaunch& K) { return launch_ns_norm(K, st); }));
+  NS_TRY(ns_rows(p, L, it, step, st));
   L.x0 = static_cast<float>(it[0].sx);
   for (int planes = 1; planes <= 2; ++planes)
     NS_TRY(ns_grouped(p, L, [=](const NsClass& c) { return c.planes == planes; }, [](const NsDesc& d, NsClass& c) {

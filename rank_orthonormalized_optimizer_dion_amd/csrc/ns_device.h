@@ -58,4 +58,23 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
+// ||D||_F from k_ns_norm's partial sums, by all of a workgroup of W wavefronts.
+template <int W>
+__device__ __forceinline__ double ns_norm(const NsLaunch& L, const NsDesc& d, double (&part)[W]) {
+  const double* parts = reinterpret_cast<const double*>(L.ws + d.oS);
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < d.parts; i += 64 * W) sum += parts[i];
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  double v[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) v[w] = part[w];
+#pragma unroll
+  for (int h = 1; h < W; h *= 2)
+#pragma unroll
+    for (int w = 0; w < W; w += 2 * h) v[w] += v[w + h];
+  return sqrt(v[0]);
+}
+
 }  // namespace dion

@@ -34,19 +34,20 @@ struct NsDesc {
   int32_t tall;
   int32_t slot;     // index in the caller's list = status word index
   int32_t parts;    // partial sums of squares
-  int32_t planes;   // 16-bit planes per value: 1 or 2
+  int32_t planes;   // as NsClass
   float scale;      // step: the update's factor lr * s
   int64_t chunk;    // elements of G per partial sum
   // pp = ns_pad(p), qp = ns_pad(q), 16-bit, `planes` per value (mm16.h),
-  // pitches ns_pitch:
+  // pitches ns_pitch (kNsFewRows: X in float32, pitch ns_row_pitch; oA, oB
+  // the chunks' sums of A in turn):
   int64_t oX;       // two buffers of pp x qp (X and the next X)
   int64_t oA, oB;   // pp x pp each: A = X X^T, B = a I + b A + c A^2
   int64_t oS;       // parts float64, then the normalization tau (float32)
 };
 
 struct NsClass {
-  int32_t planes;         // 0: the one-workgroup form
-  int32_t spp, sqp;       // its padded sides; sqp = 0: k_ns_tiny with spp >= p rows
+  int32_t planes;         // 16-bit planes per value: 1 or 2; 0: the one-workgroup form; kNsFewRows
+  int32_t spp, sqp;       // its padded sides; sqp = 0: k_ns_tiny or k_ns_rows with spp >= p rows
   int32_t first, count;   // matrices of this shape in the table
   int32_t tiles, base;    // work items per matrix, first item
   int32_t tx, ty;         // tile grid
@@ -97,6 +98,23 @@ struct NsSmall {
 constexpr int kNsTinySide = 16;
 constexpr int kNsTinyFloats = 32768;
 
+// k_ns_rows: p <= 16 beyond that.  Columns of a workgroup, at most 256
+// workgroups.
+constexpr int32_t kNsFewRows = 3;
+constexpr int kNsRowThreads = 512;
+constexpr int kNsRowChunks = 256;
+inline __host__ __device__ int ns_row_cols(int q) {
+  constexpr int unit = kNsRowThreads * kNsRowChunks;
+  return (q + unit - 1) / unit * kNsRowThreads;
+}
+inline __host__ __device__ int64_t ns_row_pitch(int q) { return (static_cast<int64_t>(q) + 63) / 64 * 64; }
+struct NsRows {
+  NsLaunch common;        // classes (tiles: chunks of columns), status, momentum, types
+  int32_t stage;          // 0: load; then iteration `stage` with a, b, c
+  int32_t steps, step;    // step: Muon step, else the output is written
+  float a, b, c;
+};
+
 struct NsUpload {
   NsDesc d[kNsUpload];
   NsDesc* dst;
@@ -108,6 +126,7 @@ hipError_t launch_ns_table(const NsUpload& u, hipStream_t st);
 hipError_t launch_ns_small(const NsSmall& L, int pp, int qp, hipStream_t st);
 // p: 1, 2, 4, 8 or 16
 hipError_t launch_ns_tiny(const NsSmall& L, int p, hipStream_t st);
+hipError_t launch_ns_rows(const NsRows& L, int p, hipStream_t st);
 hipError_t launch_ns_norm(const NsLaunch& L, hipStream_t st);
 hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st);
 // tile: 128 or 256

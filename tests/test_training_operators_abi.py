@@ -65,3 +65,13 @@ def test_columns_of_one_buffer(lib):
     # dy | dx beside each other (x elsewhere)
     assert linear(lib, "backward", x=W, dy=A, lddy=96, dx=A + 4 * 32, lddx=96) == ok
     assert linear(lib, "backward", x=W, dy=A, lddy=96, dx=A + 4 * 33, lddx=96) == no
+
+
+@pytest.mark.parametrize("p,q", [(1, 32769), (1, 1 << 20), (4, 10000), (16, 2049), (16, 100000)])
+def test_few_rows_workspace(lib, p, q):
+    """A matrix of at most 16 rows or columns takes a float32 copy of itself and
+    partial sums (less than half a megabyte), not planes padded to 64 rows."""
+    for m, n in ((p, q), (q, p)):
+        a = dion.dion_ns_matrix(A, B, m, n, n, n)
+        for math in dion.MATH_NS.values():
+            assert 0 < lib.dion_orthogonalize_workspace_size(ctypes.byref(a), 1, math) <= 8 * p * q + (1 << 19)
