@@ -1,0 +1,87 @@
+"""Orthogonalization and the Muon step (GPU) where lists mix schedules: the
+grouped launches with tiles cut along the reduction, large tiles, the
+one-workgroup forms.  Tolerances as in test_gpu_ns."""
+import pytest
+
+from .gpuhelp import say
+from .test_gpu_ns import Q, TOL16, TOL32, draw, muon64, ns64, rel
+
+pytestmark = pytest.mark.gpu
+
+TOLS = {"f32": TOL32, "f16": TOL16}
+BAD = (float("inf"), float("nan"), float("-inf"))
+# few tiles and long reductions (cut along them), one-workgroup forms, and
+# next to each a sound one; shape, whether it is bad
+MIXED = [((300, 6000), True), ((300, 6000), False), ((6000, 300), True), ((6000, 300), False), ((1500, 1700), True),
+         ((1500, 1700), False), ((520, 260), False), ((520, 260), True), ((3, 50), True), ((3, 50), False),
+         ((70, 40), True), ((70, 40), False), ((130, 1000), True), ((130, 1000), False)]
+# enough 256 x 256 tiles, one matrix bad
+MANY = [((768, 768), i == 5) for i in range(48)] + [((700, 1500), i == 2) for i in range(6)]
+
+
+def spoil(t, seed):
+    """One entry that is not finite: the first, the last, or one between."""
+    r, c = [(0, 0), (t.shape[0] - 1, t.shape[1] - 1), (t.shape[0] // 2, t.shape[1] // 3)][seed % 3]
+    t[r, c] = BAD[(seed // 3 + seed) % 3]
+
+
+def bits(t):
+    import torch
+    return t.view(torch.int32)
+
+
+@pytest.mark.parametrize("mode", ["f32", "f16"])
+@pytest.mark.parametrize("cases", [MIXED, MANY], ids=["mixed", "many"])
+def test_orthogonalize_keeps_bad_matrices_out(gpu_lib, cases, mode):
+    import torch
+    say(f"ns bad {len(cases)} {mode}")
+    n = len(cases)
+    want = [gpu_lib.STATUS_NONFINITE if bad else 0 for _, bad in cases]
+    sound = [draw(*s, 600 + i, torch.float32) for i, (s, _) in enumerate(cases)]
+    G = [g.clone() for g in sound]
+    for i, (_, bad) in enumerate(cases):
+        if bad:
+            spoil(G[i], i)
+    O = [torch.full(s, 3.0, device="cuda") for s, _ in cases]
+    ws = gpu_lib.orthogonalize_batched(list(zip(G, O)), math=mode)
+    for rep in range(2):   # the second time on the workspace that the first left
+        assert gpu_lib.status(ws, n)[1] == want
+        for i, (_, bad) in enumerate(cases):
+            if bad:
+                assert torch.all(O[i] == 3.0), i
+            elif n < 20 or i % 9 in (4, 6) or i >= 48:
+                assert rel(O[i], ns64(G[i].double(), [Q] * 5)) <= TOLS[mode], i
+            if not bad:
+                O[i].fill_(float("nan"))
+        ws = gpu_lib.orthogonalize_batched(list(zip(G, O)), math=mode, workspace=ws)
+    # and nothing of them is left when all are sound
+    gpu_lib.orthogonalize_batched(list(zip(sound, O)), math=mode, workspace=ws)
+    gpu_lib.check_status(ws, n)
+    for i in range(n):
+        if cases[i][1] or n < 20:
+            assert rel(O[i], ns64(sound[i].double(), [Q] * 5)) <= TOLS[mode], i
+
+
+@pytest.mark.parametrize("mode", ["f32", "f16"])
+@pytest.mark.parametrize("where", ["G", "M"])
+def test_muon_keeps_bad_matrices_out(gpu_lib, mode, where):
+    import torch
+    cases = MIXED + [((768, 768), False)] * 2 + [((768, 768), True)]
+    n = len(cases)
+    X = [draw(*s, 700 + i, torch.float32) * 0.02 for i, (s, _) in enumerate(cases)]
+    M = [draw(*s, 800 + i, torch.float32) for i, (s, _) in enumerate(cases)]
+    G = [draw(*s, 900 + i, torch.float32) for i, (s, _) in enumerate(cases)]
+    for i, (_, bad) in enumerate(cases):
+        if bad:
+            spoil((G if where == "G" else M)[i], i)
+    x0, m0 = [x.clone() for x in X], [m.clone() for m in M]
+    ws = gpu_lib.muon_step_batched(list(zip(X, G, M)), 0.02, 0.9, True, 0.1, 1.5, math=mode)
+    assert gpu_lib.status(ws, n)[1] == [gpu_lib.STATUS_NONFINITE if bad else 0 for _, bad in cases]
+    for i, ((m, k), bad) in enumerate(cases):
+        if bad:
+            assert torch.equal(bits(X[i]), bits(x0[i])) and torch.equal(bits(M[i]), bits(m0[i])), i
+            continue
+        x, mm = muon64(x0[i].double(), G[i].double(), m0[i].double(), 0.02, 0.9, True, 0.1, 1.5, [Q] * 5)
+        assert rel(M[i], mm) <= 2.0 ** -22
+        bound = TOLS[mode] * 0.02 * 1.5 * min(m, k) ** 0.5 * 1.2 + 2.0 ** -22 * float(torch.linalg.vector_norm(x))
+        assert float(torch.linalg.vector_norm(X[i].double() - x)) <= bound, i
