@@ -85,3 +85,45 @@ def test_muon_keeps_bad_matrices_out(gpu_lib, mode, where):
         assert rel(M[i], mm) <= 2.0 ** -22
         bound = TOLS[mode] * 0.02 * 1.5 * min(m, k) ** 0.5 * 1.2 + 2.0 ** -22 * float(torch.linalg.vector_norm(x))
         assert float(torch.linalg.vector_norm(X[i].double() - x)) <= bound, i
+
+
+def step_case(lib, shapes, mode, gdt, nesterov=True):
+    """One Muon step over a list, every matrix against float64."""
+    import torch
+    X = [draw(m, n, 20 + i, torch.float32) * 0.02 for i, (m, n) in enumerate(shapes)]
+    M = [draw(m, n, 120 + i, torch.float32) for i, (m, n) in enumerate(shapes)]
+    G = [draw(m, n, 220 + i, gdt) for i, (m, n) in enumerate(shapes)]
+    want = [muon64(x.double(), g.double(), mm.double(), 0.02, 0.95, nesterov, 0.1, 1.5, [Q] * 5)
+            for x, g, mm in zip(X, G, M)]
+    ws = lib.muon_step_batched(list(zip(X, G, M)), 0.02, 0.95, nesterov, 0.1, 1.5, math=mode)
+    lib.check_status(ws, len(shapes))
+    for s, x, mm, (ex, em) in zip(shapes, X, M, want):
+        assert rel(mm, em) <= 2.0 ** -22, s
+        bound = TOLS[mode] * 0.02 * 1.5 * min(s) ** 0.5 * 1.2 + 2.0 ** -22 * float(torch.linalg.vector_norm(ex))
+        assert float(torch.linalg.vector_norm(x.double() - ex)) <= bound, s
+
+
+@pytest.mark.parametrize("m,n", [(130, 1000), (1000, 130), (257, 129), (300, 6000), (6000, 300), (600, 520), (1031, 773)])
+@pytest.mark.parametrize("gdt", ["float32", "bfloat16"])
+def test_muon_float16_products(gpu_lib, m, n, gdt):
+    import torch
+    say(f"muon f16 {m}x{n} {gdt}")
+    for nesterov in (True, False):
+        step_case(gpu_lib, [(m, n)], "f16", getattr(torch, gdt), nesterov)
+
+
+@pytest.mark.parametrize("mode", ["f32", "f16"])
+def test_muon_large_tiles(gpu_lib, mode):
+    """256 x 256 tiles in every product, wide and tall, ragged edges: 28 upper
+    tiles of a 1543-row matrix, ten of them."""
+    import torch
+    shapes = [(1543, 1600), (1600, 1543)] * 5
+    say(f"muon large tiles {mode}")
+    step_case(gpu_lib, shapes, mode, torch.bfloat16)
+
+
+@pytest.mark.parametrize("mode", ["f32", "f16"])
+def test_muon_list_of_mixed_shapes(gpu_lib, mode):
+    import torch
+    say(f"muon mixed {mode}")
+    step_case(gpu_lib, [s for s, _ in MIXED] + [(900, 1400), (1400, 900), (2, 40000)], mode, torch.float32)
