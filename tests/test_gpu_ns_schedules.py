@@ -127,3 +127,33 @@ def test_muon_list_of_mixed_shapes(gpu_lib, mode):
     import torch
     say(f"muon mixed {mode}")
     step_case(gpu_lib, [s for s, _ in MIXED] + [(900, 1400), (1400, 900), (2, 40000)], mode, torch.float32)
+
+
+@pytest.mark.parametrize("m,n", [(4, 9), (70, 40), (130, 300), (2, 30000)])
+def test_single_matrix_entry_points(gpu_lib, m, n):
+    """dion_orthogonalize and dion_muon_step give the bits of lists of one."""
+    import ctypes
+    import torch
+    lib = gpu_lib.load()
+    coeffs = (ctypes.c_float * 15)(*(Q * 5))
+    stream = torch.cuda.current_stream().cuda_stream
+    for mode in ("f32", "f16"):
+        for gdt in (torch.float32, torch.bfloat16):
+            big = draw(m, n + 3, 1, gdt)
+            G, g = big[:, :n], 1 if gdt == torch.bfloat16 else 0
+            for odt in (torch.float32, torch.bfloat16):
+                want = torch.empty(m, n, dtype=odt, device="cuda")
+                ws = gpu_lib.orthogonalize(G, want, math=mode)
+                got = torch.zeros(m, n + 1, dtype=odt, device="cuda")
+                rc = lib.dion_orthogonalize(big.data_ptr(), n + 3, got.data_ptr(), n + 1, m, n, coeffs, 5,
+                                            gpu_lib.MATH_NS[mode], g, 1 if odt == torch.bfloat16 else 0,
+                                            ws.data_ptr(), ws.numel(), stream)
+                assert rc == gpu_lib.OK and torch.equal(got[:, :n], want)
+                assert torch.count_nonzero(got[:, n]) == 0
+            G = G.contiguous()
+            X, M = draw(m, n, 2, torch.float32), draw(m, n, 3, torch.float32)
+            x, mm = X.clone(), M.clone()
+            ws = gpu_lib.muon_step(X, G, M, 0.02, 0.9, True, 0.1, 0.7, math=mode)
+            rc = lib.dion_muon_step(x.data_ptr(), G.data_ptr(), mm.data_ptr(), m, n, 0.7, 0.02, 0.9, 1, 0.1, coeffs,
+                                    5, gpu_lib.MATH_NS[mode], g, ws.data_ptr(), ws.numel(), stream)
+            assert rc == gpu_lib.OK and torch.equal(X, x) and torch.equal(M, mm)
