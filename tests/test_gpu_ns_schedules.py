@@ -157,3 +157,21 @@ def test_single_matrix_entry_points(gpu_lib, m, n):
             rc = lib.dion_muon_step(x.data_ptr(), G.data_ptr(), mm.data_ptr(), m, n, 0.7, 0.02, 0.9, 1, 0.1, coeffs,
                                     5, gpu_lib.MATH_NS[mode], g, ws.data_ptr(), ws.numel(), stream)
             assert rc == gpu_lib.OK and torch.equal(X, x) and torch.equal(M, mm)
+
+
+@pytest.mark.parametrize("mode", ["f32", "f16"])
+def test_many_shapes(gpu_lib, mode):
+    """61 matrices, each of its own shape, in every form: three uploads of the
+    descriptor table and several launches per product."""
+    import torch
+    shapes = [(3 + 17 * i, 5 + (29 * i * i) % 1100) for i in range(45)]
+    shapes += [(2 + i, 20000 - 900 * i) for i in range(8)] + [(17000 + i, 1 + 2 * i) for i in range(8)]
+    assert len(set(shapes)) == 61
+    say(f"ns many shapes {mode}")
+    G = [draw(m, n, 1000 + i, torch.float32) for i, (m, n) in enumerate(shapes)]
+    O = [torch.full(s, float("nan"), device="cuda") for s in shapes]
+    ws = gpu_lib.orthogonalize_batched(list(zip(G, O)), math=mode)
+    gpu_lib.check_status(ws, len(shapes))
+    for s, g, o in zip(shapes, G, O):
+        assert rel(o, ns64(g.double(), [Q] * 5)) <= TOLS[mode], s
+    step_case(gpu_lib, shapes, mode, torch.bfloat16)
