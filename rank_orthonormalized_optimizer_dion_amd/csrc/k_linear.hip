@@ -43,7 +43,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
 
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
-    case DION_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case DION_ACT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
     case DION_ACT_RELU2: return z > 0.0f || z != z ? 2.0f * z : 0.0f;
     case DION_ACT_GELU:
       return normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);

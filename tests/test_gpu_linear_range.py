@@ -152,3 +152,21 @@ def test_orthogonalize_beside_its_input(gpu_lib):
         gpu_lib.orthogonalize(g0, want)
         gpu_lib.orthogonalize(buf[:, :n], buf[:, n:])
         assert torch.equal(buf[:, n:], want) and torch.equal(buf[:, :n], g0)
+
+
+@pytest.mark.parametrize("act", ["relu", "relu2", "gelu", "silu"])
+def test_nan_preactivation_shows_in_the_gradients(gpu_lib, act):
+    """A NaN pre-activation (a non-finite operand) makes its row of dx, its
+    rows of dw and its entry of db NaN, and nothing else."""
+    import torch
+    for dtype in (torch.float32, torch.bfloat16):
+        for t in (4, 40, 130):
+            g = torch.Generator(device="cuda").manual_seed(t)
+            x, w = torch.randn(t, 80, generator=g, device="cuda").to(dtype), torch.randn(48, 80, generator=g, device="cuda").to(dtype)
+            dy, z = (torch.randn(t, 48, generator=g, device="cuda").to(dtype) for _ in range(2))
+            z[2, 7] = float("nan")
+            dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(48, device="cuda")
+            gpu_lib.linear_backward(dy, x, w, dx=dx, dw=dw, db=db, act=act, preact=z)
+            for v, at in ((dx, 2), (dw, 7), (db.view(48, 1), 7)):
+                assert torch.isnan(v[at]).all()
+                assert torch.isfinite(v).all(1).sum() == v.shape[0] - 1
