@@ -326,7 +326,8 @@ int dion_status(const void* workspace, int count, void* stream, int* per_matrix)
  *   quintic iterations of an N(0, 1) matrix, below bfloat16's own rounding of
  *   the result, growing for matrices whose singular values fall off steeply.
  *   A matrix whose smaller side is at most 128 keeps float32 accuracy in both
- *   (its roundings would average over too few singular values).  Entries are
+ *   (its roundings would average over too few singular values), one of at most
+ *   16 rows or columns is computed in plain float32.  Entries are
  *   held relative to the largest singular value that the coefficients allow:
  *   coefficients that shrink everything far below it lose accuracy.
  *
@@ -334,9 +335,9 @@ int dion_status(const void* workspace, int count, void* stream, int* per_matrix)
  * step, a non-finite momentum) sets DION_STATUS_NONFINITE in its status word
  * (dion_status) and leaves O, or X and M, as they were.  The conventions at
  * the top of this header hold, with these differences: G and O have row
- * pitches ldg, ldo >= n (elements) and may be column blocks of one buffer, of
- * one pitch; m, n >= 1 with m n < 2^31 and any order; a list holds at most
- * DION_MAX_LIST matrices.  The list is read before the
+ * pitches ldg, ldo >= n (elements, < 2^31) and may be column blocks of one
+ * buffer, of one pitch; 1 <= m, n <= DION_MAX_DIM with m n < 2^31 and any order;
+ * a list holds at most DION_MAX_LIST matrices.  The list is read before the
  * call returns.  The same call gives the same bits; a matrix's last bits may
  * depend on the other matrices of the list (long sums are cut to fill the
  * chip). */
@@ -394,17 +395,16 @@ int dion_muon_step(float* X, const void* G, float* M, int64_t m, int64_t n, floa
  * (the residual's gradient is dy itself).  dW is the G that a step reads.
  *
  * Every tensor has `dtype` (float32 or bfloat16) except bias and db, which
- * are float32, and a row pitch in elements (>= its columns); any alignment of
- * its elements and any t >= 0 (t = 0: dW and db are zero).  bfloat16 products
- * are exact and summed in float32; act, bias and residual are applied in
- * float32 and the result is rounded once; backward rounds dz to bfloat16
- * before the two products when there is an activation and more than 64
- * tokens.  float32 products are
- * taken as six bfloat16 products of three-way split operands (24 bits, errors
- * of float32's order; with more than 8 tokens, and in the backward pass, a
- * value below 2^-110 is taken to within 2^-134); a non-finite operand makes
- * the outputs it reaches non-finite, not always with the sign float32 would
- * give.
+ * are float32, and a row pitch in elements (>= its columns, <= 2^30); elements
+ * in their natural alignment, n, k <= DION_MAX_DIM and 0 <= t <= 2^24 (t = 0: dW
+ * and db are zero).  bfloat16 products are exact and summed in float32; act,
+ * bias and residual are applied in float32 and the result is rounded once;
+ * backward of bfloat16 with an activation rounds dz to bfloat16 before the two
+ * products (to 16 bits with at most 64 tokens).  float32 products are taken as
+ * six bfloat16 products of three-way split operands (24 bits, errors of
+ * float32's order; with more than 8 tokens, and in the backward pass, a value
+ * below 2^-110 is taken to within 2^-134); a non-finite operand makes the
+ * outputs it reaches non-finite, not always with the sign float32 would give.
  *
  * Forward reads x, w, bias (or NULL), residual (or NULL; y itself is allowed)
  * and writes y and, when z is not NULL, z.  Backward reads dy, z (only with

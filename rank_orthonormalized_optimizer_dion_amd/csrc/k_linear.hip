@@ -14,10 +14,12 @@
 // (below, the planes end at 2^-133).
 //
 // Bound and measured (MI355X): large batches by the matrix cores (8192
-// tokens, 8192 -> 3072 with GELU, bias and residual: 438 us, 0.94 PFLOP/s; the
+// tokens, 8192 -> 3072 with GELU, bias and residual: 432 us, 0.95 PFLOP/s; the
 // backward of 3072 -> 8192: 0.93 ms, 0.89 PFLOP/s), one token by streaming W
-// (3072 -> 8192: 12.0 us, 4.2 TB/s), float32 by the six products of its split
-// planes (1021 tokens, 773 -> 2051, backward: 137 us).
+// (3072 -> 8192: 11.9 us, 4.2 TB/s), float32 by the six products of its split
+// planes (1021 tokens, 773 -> 2051, backward: 133 us) and, with few tokens, by
+// writing and sweeping the weight's planes (9 tokens, 3072 -> 8192: 101 us; 8
+// tokens without them: 52 us).
 #include "dion.h"
 #include "linear_types.h"
 #include "mm16.h"

@@ -17,9 +17,9 @@
 //
 // Bound and measured (MI355X): large matrices by the matrix cores at the
 // clock the power limit leaves (8192 x 28672, float16, five quintic
-// iterations: 27.6 to 28.2 ms, 1.12 PFLOP/s of algorithmic work; one layer of the 3B
-// stack, float32: 15.8 ms, 0.98 PFLOP/s of matrix-core products); 768-row
-// stacks by each tile's prologue and epilogue (six layers, float16: 1.03 to 1.05 ms);
+// iterations: 27.7 ms, 1.14 PFLOP/s of algorithmic work; one layer of the 3B
+// stack, float32: 15.4 ms, 1.01 PFLOP/s of matrix-core products); 768-row
+// stacks by each tile's prologue and epilogue (six layers, float16: 0.98 to 1.05 ms);
 // a few matrices by launch latency (five of about 1500 x 500: 0.26 ms in 18
 // launches).
 #include "mm16.h"

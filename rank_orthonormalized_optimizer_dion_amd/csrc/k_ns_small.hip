@@ -236,7 +236,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_ns_small(NsSmall L) {
   for (int it = 0; it < L.steps; ++it) {
     // a lane number that is new in every iteration: the hundreds of LDS and
     // output addresses made from it would otherwise be computed once, before
-    // the loop, and spilled
+    // the loop, and spilled (the 64 x 512 and 128 x 256 forms still spill six to
+    // ten registers)
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const NsSmall::Iter s = L.it[it];

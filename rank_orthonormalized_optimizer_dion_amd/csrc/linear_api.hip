@@ -27,7 +27,12 @@ constexpr int64_t kLinDirectPitch = int64_t{1} << 22;
 // tokens it takes two planes (hi + lo) instead: its roundings average over
 // too few terms there, and the products' time is the weights' traffic.
 constexpr int kLinFewTokens = 64;
-constexpr int64_t kLinBigTiles = 256;   // 256 x 256 tiles in a product of at least this many
+// 256 x 256 tiles in a product of at least this many (one per CU), else 128 x
+// 128.  Timed in bfloat16: 4096 tokens, 4096 -> 4096 110 us, with 128 x 128 163
+// us; backward, 4096 tokens, 3072 -> 3072 (144 and 192 tiles) 257 us, with 256 x 256 227
+// us.  The count is of padded tiles: 100 tokens, 768 -> 66000 take 46 us, with
+// 128 x 128 31 us.
+constexpr int64_t kLinBigTiles = 256;
 
 bool span_ok(const Span& s, bool required) {
   if (!s.p) return !required || s.rows == 0;

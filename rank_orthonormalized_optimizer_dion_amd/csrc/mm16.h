@@ -15,14 +15,16 @@
 // Tiles go from global memory straight to LDS (global_load_lds, 16 bytes per
 // lane), no registers and no conversion.  A wavefront's 64 lanes write 64
 // consecutive 16-byte cells, so a swizzle can only permute which cell of the
-// source each lane fetches.  The LDS serves 16 lanes' ds_read_b128 at a time
-// from 64 banks, so 16 consecutive lanes have to cover 16 different cells
-// modulo 16 (with rows of 4 cells and no swizzle half the reads' cycles were
-// bank conflicts):
+// source each lane fetches.  64 banks serve 16 cells at a time; the
+// permutations let 16 consecutive lanes cover 16 different cells modulo 16:
 //   K-major: cell (x, c) of a row of 4 cells sits at 4 x + (c ^ (x / 4) % 4);
 //   x-major: cell (k, c), c = x / 8, sits at k CPR + (c ^ (4 (k % 4) + 2
 //     (k / 8 % 2))); ds_read_b64_tr_b16 transposes 4 k by 16 x blocks on the
 //     way out.
+// Counted (share of the LDS's working cycles lost to conflicts): x-major tiles
+// of one plane 1%, K-major tiles of two planes 2%; K-major tiles of one plane
+// 50% (a read takes four cells of 16 rows there, two of 32 rows with two
+// planes), and products with an x-major tile of two planes 33%.
 #pragma once
 #include <type_traits>
 

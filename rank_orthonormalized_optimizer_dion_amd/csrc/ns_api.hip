@@ -24,7 +24,13 @@ namespace {
 // came out 4.6e-3 off with one plane, where large ones are 1.2e-3 off), and
 // launches, not products, are its cost.
 constexpr int kNsSmallSide = 128;
-constexpr int64_t kNsBigTiles = 256;   // 256 x 256 tiles in a launch of at least this many
+// 256 x 256 tiles in a launch of at least this many (one per CU), else 128 x
+// 128.  Timed, float16 unless said: always 128: 4096 x 4096 1.84 ms (1.60),
+// 3072 x 8192 1.94 ms (1.86), twelve of 1543 x 1543 1.73 ms (1.83); from 64 tiles
+// on: 3072 x 8192 1.70 ms, but 2048 x 2048 float32 0.91 ms (0.80).  The count is
+// of padded tiles: matrices of few rows, which fill a fraction of theirs, lose
+// by it (300 of 64 x 768: 0.94 ms, 0.71 with 128 x 128).
+constexpr int64_t kNsBigTiles = 256;
 static_assert(kNsCounts >= kTileSlots128 && kNsCounts >= kTileSlots256, "arrival counters");
 constexpr size_t kNsAlign = 256;
 size_t ns_align(size_t x) { return (x + kNsAlign - 1) / kNsAlign * kNsAlign; }
