@@ -304,10 +304,12 @@ NsSmall ns_small_args(const NsLaunch& L, const std::vector<NsIter>& it, bool ste
 
 // The stages of k_ns_rows, over the matrices of each number of rows.
 hipError_t ns_rows(const NsPlan& p, const NsLaunch& base, const std::vector<NsIter>& it, bool step, hipStream_t st) {
+  const auto few = [](const NsClass& c) { return c.planes == kNsFewRows; };
+  if (std::none_of(p.shapes.begin(), p.shapes.end(), few)) return hipSuccess;
   const int steps = static_cast<int>(it.size());
   for (int stage = 0; stage <= steps; ++stage)
     for (const int rows : {1, 2, 4, 8, 16})
-      NS_TRY(ns_grouped(p, base, [=](const NsClass& c) { return c.planes == kNsFewRows && c.spp == rows; },
+      NS_TRY(ns_grouped(p, base, [=](const NsClass& c) { return few(c) && c.spp == rows; },
                         [](const NsDesc& d, NsClass& c) { c.tiles = ns_row_chunks(d.q); },
                         [&](const NsLaunch& K) {
                           const NsIter s = stage > 0 ? it[stage - 1] : NsIter{};
