@@ -74,8 +74,13 @@ struct LinSkinny {
   LinOut out;
 };
 
-constexpr int kSkinnyTokens = 64;   // matrix-core kernel for few tokens
-constexpr int kRowTokens = 8;       // float32 / unaligned kernel for few tokens
+// k_lin_skinny up to this many tokens, tiles beyond.  Timed both ways: 17 to 33
+// tokens 2% to 39% faster than tiles (17: 3072 -> 8192 15.2 us against 24.9); 64
+// tokens 768 -> 768 10.5 us against 12.2, but 8192 -> 3072 37.7 us against 29.4.
+constexpr int kSkinnyTokens = 64;
+// k_lin_rows (float32, or rows not 16-byte aligned) up to this many: 8 tokens
+// of float32 3072 -> 8192 52 us, as split planes on tiles 100 us.
+constexpr int kRowTokens = 8;
 
 hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st);
 hipError_t launch_lin_packs(const LinPacks& p, hipStream_t st);

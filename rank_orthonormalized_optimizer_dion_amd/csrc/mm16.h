@@ -255,7 +255,8 @@ __device__ __forceinline__ void interleave16() {
 // always has a cluster whose operands are in registers when it reaches the
 // barrier.  Two wavefronts per SIMD (256 x 256 tiles, 4 stages) or two
 // workgroups per CU (128 x 128, 4 stages) fill each other's gaps; a launch
-// of too few 128 x 128 tiles for that takes 8 stages.
+// of too few 128 x 128 tiles for that takes 8 stages (against 4: the linear
+// layer from 3% faster to 2% slower, Newton-Schulz lists 1% to 3% slower).
 // kend - kbeg is a multiple of a stage's k.
 template <class S, class Seg>
 __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typename S::B& tb,
