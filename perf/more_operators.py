@@ -122,8 +122,9 @@ def run(state):
 def _run_own(s, case):
     import rank_orthonormalized_optimizer_dion_amd as dion
     if case["op"] == "adamw":
-        dion.adamw_step_batched(s["list"], LR, STEP, betas=(BETA1, BETA2), eps=EPS, weight_decay=s["wd"],
-                                grad_scale=s["scale"], seed=SEED)
+        if "plan" not in s:
+            s["plan"] = dion.AdamWPlan(s["list"], weight_decay=s["wd"])
+        s["plan"].step(LR, STEP, betas=(BETA1, BETA2), eps=EPS, grad_scale=s["scale"], seed=SEED)
         return _adamw_outputs(s)
     kw = dict(ignore_index=IGNORE, label_smoothing=case["smoothing"], z_loss=case["z_loss"], workspace=s.get("ws"))
     if case["op"] == "forward":
