@@ -442,6 +442,65 @@ int dion_linear_forward(const dion_linear* l, void* workspace, size_t workspace_
 size_t dion_linear_backward_workspace_size(const dion_linear* l);
 int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * AdamW step for the tensors that the matrix steps above leave alone
+ * (embeddings, output heads, norms, biases): for each tensor of n elements,
+ * in any order, with g = c G and step t >= 1,
+ *   m <- beta1 m + (1 - beta1) g
+ *   v <- beta2 v + (1 - beta2) g^2
+ *   X <- (1 - lr weight_decay) X
+ *        - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * c = *grad_scale, one float32 on the device (a clipping factor or the inverse
+ * of a loss scale, say), or 1 where grad_scale is NULL.  A c that is not
+ * finite leaves every tensor as it was.
+ *
+ * state_bits: the moments' form.
+ *   DION_STATE_F32   M and V hold m and v in float32; S is not used.
+ *   DION_STATE_8BIT  M and V hold m and sqrt(v), one byte per element, in
+ *     blocks of DION_ADAMW_BLOCK consecutive elements: an e4m3 value (4 bits of
+ *     exponent, 3 of mantissa, no infinities) times the block's scale, a power
+ *     of two 2^(b - 127).  S holds the bytes b: first M's, one per block (the
+ *     last block may be short), then V's.  All zero is the state before the
+ *     first step.  X is stepped with the new moments before they are rounded.
+ *     b is the exponent byte of the block's largest magnitude less 7, at
+ *     least 1, and a scaled magnitude a < 256 is rounded to floor(a / ulp + u)
+ *     ulp, ulp = 2^(max(floor(log2 a), -6) - 3), whose mean over u in [0, 1) is
+ *     a: moments move by far less than an ulp per step.  A nonzero sqrt(v) is
+ *     never rounded to zero (a moment without its v would be divided by eps).
+ *     u comes from the caller's seed, which should differ from step to step,
+ *     and the element's index i in its tensor (mod 2^32):
+ *       h = (i + 0x632be5ab seed) 0x9e3779b1;  h = (h ^ h / 2^15) 0x85ebca77;
+ *       h = h ^ h / 2^13;  u = h mod 2^16 (M), h / 2^16 (V), over 2^16
+ *     A block with a new m or v that is not finite becomes NaN as a whole.
+ *
+ * Everything else that is not finite reaches the elements it belongs to.
+ * Tensors of a list share no memory; X, M, V, S and G of one do not overlap.
+ * Pointers in their elements' alignment (16 bytes are faster), 0 <= n <= 2^36
+ * (n = 0: pointers are not looked at), float32 X, G of one type for the list, at
+ * most DION_MAX_LIST tensors.  0 <= beta1, beta2 < 1; lr, weight_decay finite;
+ * 1.2e-38 <= eps <= 1e30.  The list is read before the call returns; no
+ * workspace; the same call gives the same bits. */
+#define DION_STATE_F32   32
+#define DION_STATE_8BIT  8
+#define DION_ADAMW_BLOCK 64
+
+typedef struct dion_adamw_tensor {
+  float*      X;        /* n, updated in place */
+  const void* G;        /* n, float32 or bfloat16 per g_dtype, read only */
+  void*       M;        /* n float32 or n bytes, updated in place */
+  void*       V;        /* n float32 or n bytes, updated in place */
+  uint8_t*    S;        /* 2 ceil(n / DION_ADAMW_BLOCK) bytes, updated in place, or NULL */
+  int64_t     n;
+  double      weight_decay;
+} dion_adamw_tensor;
+
+int dion_adamw_step_batched(const dion_adamw_tensor* tensors, int count, double lr, double beta1,
+                            double beta2, double eps, int64_t step, const float* grad_scale,
+                            int state_bits, uint32_t seed, int g_dtype, void* stream);
+int dion_adamw_step(float* X, const void* G, void* M, void* V, uint8_t* S, int64_t n, double lr,
+                    double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                    const float* grad_scale, int state_bits, uint32_t seed, int g_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,7 @@ __all__ = [
     "workspace_size_batched", "step", "step_batched", "step_noalloc", "status",
     "check_status", "version", "VARIANTS", "NS_COEFFS", "orthogonalize", "orthogonalize_batched",
     "muon_step", "muon_step_batched", "linear_forward", "linear_backward", "ACTS",
+    "adamw_step", "adamw_step_batched", "AdamWPlan", "adamw_state8",
 ]
 
 OK = 0
@@ -45,6 +46,7 @@ STATUS_ORTH_P, STATUS_ORTH_W, STATUS_COLNORM = 1, 2, 4
 STATUS_NONFINITE = 8   # orthogonalize, muon_step: non-finite input
 MATH_NS = {"f32": 0x0000, "f16": 0x1000}   # orthogonalize, muon_step
 ACTS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}   # linear_forward / _backward
+ADAMW_BLOCK = 64   # elements that share the scales of an 8-bit state
 # the quintic Newton-Schulz coefficients in common use
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
@@ -101,6 +103,12 @@ class dion_linear(ctypes.Structure):
                 ("act", ctypes.c_int), ("dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
 
 
+class dion_adamw_tensor(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("G", ctypes.c_void_p), ("M", ctypes.c_void_p),
+                ("V", ctypes.c_void_p), ("S", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double)]
+
+
 def load() -> ctypes.CDLL:
     """Load libdion.so (built by ``build.py``); raises if it is missing."""
     global _LIB
@@ -117,7 +125,7 @@ def load() -> ctypes.CDLL:
     mats_p = ctypes.POINTER(dion_matrix)
     ns_p, muon_p, f_p = (ctypes.POINTER(dion_ns_matrix), ctypes.POINTER(dion_muon_matrix),
                          ctypes.POINTER(ctypes.c_float))
-    lin_p = ctypes.POINTER(dion_linear)
+    lin_p, c_d = ctypes.POINTER(dion_linear), ctypes.c_double
     sig = {
         "dion_version": (c_int, []),
         "dion_error_string": (ctypes.c_char_p, [c_int]),
@@ -156,6 +164,10 @@ def load() -> ctypes.CDLL:
         "dion_linear_forward": (c_int, [lin_p, vp, c_size, vp]),
         "dion_linear_backward_workspace_size": (c_size, [lin_p]),
         "dion_linear_backward": (c_int, [lin_p, vp, c_size, vp]),
+        "dion_adamw_step_batched": (c_int, [ctypes.POINTER(dion_adamw_tensor), c_int, c_d, c_d, c_d,
+                                            c_d, c_i64, vp, c_int, ctypes.c_uint32, c_int, vp]),
+        "dion_adamw_step": (c_int, [vp, vp, vp, vp, vp, c_i64, c_d, c_d, c_d, c_d, c_d, c_i64, vp,
+                                    c_int, ctypes.c_uint32, c_int, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -714,3 +726,107 @@ def linear_backward(dy, x=None, weight=None, dx=None, dw=None, db=None, act="non
     _put(s, "dw", "lddw", dw, (n, k), dy.dtype, dev)
     _put_vector(s, "db", db, n, dev)
     return _linear("backward", s, dev, workspace, stream)
+
+
+# --- AdamW step ---------------------------------------------------------------
+
+def adamw_state8(X):
+    """The 8-bit state of X before its first step: (M, V, S), all zero."""
+    torch = _torch()
+    n = X.numel()
+    codes = [torch.zeros(X.shape, dtype=torch.uint8, device=X.device).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    scales = torch.zeros(2 * (-(-n // ADAMW_BLOCK)), dtype=torch.uint8, device=X.device)
+    return codes[0], codes[1], scales.view(torch.float8_e8m0fnu)
+
+
+class AdamWPlan:
+    """An AdamW step over a fixed list of tensors: their checks and table once,
+    for many steps."""
+
+    def __init__(self, tensors: Sequence[Tuple], weight_decay=0.0):
+        """tensors: (X, G, M, V), M and V float32, or (X, G, M, V, S), M and V
+        float8_e4m3fn and S float8_e8m0fnu (``adamw_state8``); one kind and one
+        type of G for the list.  Contiguous tensors of any shape; X, M, V and S
+        are updated in place.  weight_decay: a number, or one per tensor."""
+        torch = _torch()
+        count = len(tensors)
+        if count == 0:
+            raise ValueError("empty tensor list")
+        decays = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
+        if len(decays) != count:
+            raise ValueError("weight_decay must be a number or one per tensor")
+        first = tensors[0]
+        if len(first) not in (4, 5):
+            raise ValueError("tensors must be (X, G, M, V) or (X, G, M, V, S)")
+        self.state_bits = 8 if len(first) == 5 else 32
+        self.device = dev = first[0].device
+        gtype = first[1].dtype
+        if gtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("G must be float32 or bfloat16")
+        stype = torch.float8_e4m3fn if self.state_bits == 8 else torch.float32
+        types = (torch.float32, gtype, stype, stype, torch.float8_e8m0fnu)
+        table = (dion_adamw_tensor * count)()
+        for i, (entry, decay) in enumerate(zip(tensors, decays)):
+            if len(entry) != len(first):
+                raise ValueError("every state of a list must have the same form")
+            X = entry[0]
+            n, shape = X.numel(), X.shape
+            for name, t, kind in zip("XGMVS", entry, types):
+                if not t.is_cuda or t.device != dev:
+                    raise ValueError(f"{name} must be a GPU tensor on the first X's device")
+                if t.dtype != kind:
+                    raise TypeError(f"{name} must be {kind}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                if name == "S":
+                    if t.numel() != 2 * (-(-n // ADAMW_BLOCK)):
+                        raise ValueError(f"S must have {2 * (-(-n // ADAMW_BLOCK))} elements")
+                elif t.shape != shape:
+                    raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, X is {tuple(shape)}")
+            S = entry[4].data_ptr() if len(entry) == 5 else None
+            table[i] = (X.data_ptr(), entry[1].data_ptr(), entry[2].data_ptr(), entry[3].data_ptr(), S, n,
+                        float(decay))
+        self._tensors = [tuple(e) for e in tensors]   # keep the tensors alive
+        self._table, self.count = table, count
+        self._gdtype = 1 if gtype == torch.bfloat16 else 0
+        self._run = load().dion_adamw_step_batched
+
+    def step(self, lr: float, step: int, betas=(0.9, 0.999), eps: float = 1e-8, grad_scale=None,
+             seed: Optional[int] = None, stream=None):
+        """Step number `step` (1, 2, ...); dion_adamw_step_batched.
+
+        grad_scale: None, or a float32 GPU tensor of one element that every G is
+        multiplied by; one that is not finite skips the step on the device.
+        seed: of the 8-bit states' rounding, an integer taken modulo 2^32
+        (default: `step`)."""
+        if grad_scale is not None and (not grad_scale.is_cuda or grad_scale.device != self.device or
+                                       grad_scale.dtype != _torch().float32 or grad_scale.numel() != 1):
+            raise ValueError("grad_scale must be a float32 tensor of one element on the same device")
+        args = (self._table, self.count, float(lr), float(betas[0]), float(betas[1]), float(eps), int(step),
+                None if grad_scale is None else grad_scale.data_ptr(), self.state_bits,
+                (int(step) if seed is None else int(seed)) & 0xffffffff, self._gdtype,
+                _stream_handle(stream, self.device))
+        torch = _torch()
+        if torch.cuda.current_device() == self.device.index:
+            rc = self._run(*args)
+        else:
+            with torch.cuda.device(self.device):
+                rc = self._run(*args)
+        if rc != OK:
+            raise _err(rc)
+
+
+def adamw_step_batched(tensors: Sequence[Tuple], lr: float, step: int, betas=(0.9, 0.999),
+                       eps: float = 1e-8, weight_decay=0.0, grad_scale=None,
+                       seed: Optional[int] = None, stream=None):
+    """One AdamW step over a list of (X, G, M, V) or (X, G, M, V, S): see
+    ``AdamWPlan``, which serves many steps over the same tensors."""
+    AdamWPlan(tensors, weight_decay).step(lr, step, betas, eps, grad_scale, seed, stream)
+
+
+def adamw_step(X, G, M, V, lr: float, step: int, S=None, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay: float = 0.0, grad_scale=None, seed: Optional[int] = None, stream=None):
+    """``adamw_step_batched`` of one tensor."""
+    entry = (X, G, M, V) if S is None else (X, G, M, V, S)
+    adamw_step_batched([entry], lr, step, betas, eps, weight_decay, grad_scale, seed, stream)
