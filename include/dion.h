@@ -443,6 +443,64 @@ size_t dion_linear_backward_workspace_size(const dion_linear* l);
 int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Softmax cross entropy of an output head: the product of the hidden states
+ * with the head's weight, the loss and its gradients, without keeping the
+ * logits.  x is t x k (tokens by inputs), W n x k (n: the vocabulary), y the
+ * targets, e label_smoothing, zc z_loss:
+ *   forward:   z = x W^T;  lse = log sum_j exp z_j
+ *              loss = lse - (1 - e) z_y - e mean_j z_j + zc lse^2
+ *   backward:  dz_j = dloss ((1 + 2 zc lse) exp(z_j - lse) - (1 - e) [j = y]
+ *                            - e / n)
+ *              dx = dz W;  dW = dz^T x
+ * per token; dloss is the loss's gradient per token (1 over their number for a
+ * mean, say).  A row whose target is ignore_index has loss 0 and dz 0 whatever
+ * its logits are (its x still meets that zero in dW: a non-finite x there makes
+ * dW NaN); any other target outside 0 .. n - 1 makes its row's loss, and what
+ * its dz reaches, NaN.  dW is a G for the steps above.
+ *
+ * x, w, dx, dw have `dtype` (float32 or bfloat16) and a row pitch in elements
+ * (>= k, <= 2^30); target is int64, loss, lse and dloss float32, t contiguous
+ * elements each; elements in their natural alignment, n, k <= DION_MAX_DIM,
+ * 0 <= t <= 2^24 (t = 0: dW is zero), 0 <= e <= 1.  Products are taken as the
+ * linear layer takes them (bfloat16 exact, float32 as six bfloat16 products),
+ * sums in float32; dz is rounded to bfloat16 before its two products (to 16
+ * bits with at most 64 tokens, to 24 in float32) and computed a piece of the
+ * vocabulary at a time, so that the workspace stays near 256 MiB plus, in
+ * bfloat16, t x k float32 where there are several pieces, plus copies of
+ * operands that the tiles cannot read in place.  Forward keeps at most an eighth
+ * of a byte per logit (one and a half times that with label smoothing), few
+ * tokens up to half a byte.
+ *
+ * Forward reads x, w, target and writes those of loss and lse that are not
+ * NULL.  Backward reads x, w, target, lse (forward's) and dloss and writes
+ * those of dx and dw that are not NULL; with accumulate != 0, dw is added to.
+ * Outputs share no element with anything else.  Sums are taken in a fixed
+ * order: the same call gives the same bits.  Size queries return 0 for invalid
+ * arguments; errors as for the calls above. */
+typedef struct dion_cross_entropy {
+  int64_t        t, n, k;
+  const void*    x;         int64_t ldx;   /* t x k */
+  const void*    w;         int64_t ldw;   /* n x k */
+  const int64_t* target;                   /* t */
+  float*         loss;                     /* t */
+  float*         lse;                      /* t */
+  const float*   dloss;                    /* t */
+  void*          dx;        int64_t lddx;  /* t x k */
+  void*          dw;        int64_t lddw;  /* n x k */
+  int64_t        ignore_index;
+  float          label_smoothing, z_loss;
+  int            dtype;                    /* DION_DTYPE_* */
+  int            accumulate;
+} dion_cross_entropy;
+
+size_t dion_cross_entropy_forward_workspace_size(const dion_cross_entropy* a);
+int dion_cross_entropy_forward(const dion_cross_entropy* a, void* workspace, size_t workspace_bytes,
+                               void* stream);
+size_t dion_cross_entropy_backward_workspace_size(const dion_cross_entropy* a);
+int dion_cross_entropy_backward(const dion_cross_entropy* a, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
  * AdamW step for the tensors that the matrix steps above leave alone
  * (embeddings, output heads, norms, biases): for each tensor of n elements,
  * in any order, with g = c G and step t >= 1,

@@ -26,7 +26,7 @@ __all__ = [
     "workspace_size_batched", "step", "step_batched", "step_noalloc", "status",
     "check_status", "version", "VARIANTS", "NS_COEFFS", "orthogonalize", "orthogonalize_batched",
     "muon_step", "muon_step_batched", "linear_forward", "linear_backward", "ACTS",
-    "adamw_step", "adamw_step_batched", "AdamWPlan", "adamw_state8",
+    "cross_entropy_forward", "cross_entropy_backward", "adamw_step", "adamw_step_batched", "AdamWPlan", "adamw_state8",
 ]
 
 OK = 0
@@ -103,6 +103,19 @@ class dion_linear(ctypes.Structure):
                 ("act", ctypes.c_int), ("dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
 
 
+class dion_cross_entropy(ctypes.Structure):
+    _fields_ = [("t", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("target", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("dloss", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64),
+                ("label_smoothing", ctypes.c_float), ("z_loss", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
+
+
 class dion_adamw_tensor(ctypes.Structure):
     _fields_ = [("X", ctypes.c_void_p), ("G", ctypes.c_void_p), ("M", ctypes.c_void_p),
                 ("V", ctypes.c_void_p), ("S", ctypes.c_void_p), ("n", ctypes.c_int64),
@@ -126,6 +139,7 @@ def load() -> ctypes.CDLL:
     ns_p, muon_p, f_p = (ctypes.POINTER(dion_ns_matrix), ctypes.POINTER(dion_muon_matrix),
                          ctypes.POINTER(ctypes.c_float))
     lin_p, c_d = ctypes.POINTER(dion_linear), ctypes.c_double
+    xent_p = ctypes.POINTER(dion_cross_entropy)
     sig = {
         "dion_version": (c_int, []),
         "dion_error_string": (ctypes.c_char_p, [c_int]),
@@ -164,6 +178,10 @@ def load() -> ctypes.CDLL:
         "dion_linear_forward": (c_int, [lin_p, vp, c_size, vp]),
         "dion_linear_backward_workspace_size": (c_size, [lin_p]),
         "dion_linear_backward": (c_int, [lin_p, vp, c_size, vp]),
+        "dion_cross_entropy_forward_workspace_size": (c_size, [xent_p]),
+        "dion_cross_entropy_forward": (c_int, [xent_p, vp, c_size, vp]),
+        "dion_cross_entropy_backward_workspace_size": (c_size, [xent_p]),
+        "dion_cross_entropy_backward": (c_int, [xent_p, vp, c_size, vp]),
         "dion_adamw_step_batched": (c_int, [ctypes.POINTER(dion_adamw_tensor), c_int, c_d, c_d, c_d,
                                             c_d, c_i64, vp, c_int, ctypes.c_uint32, c_int, vp]),
         "dion_adamw_step": (c_int, [vp, vp, vp, vp, vp, c_i64, c_d, c_d, c_d, c_d, c_d, c_i64, vp,
@@ -651,20 +669,21 @@ def _put(s, name, ld, tensor, shape, dtype, device):
     setattr(s, ld, pitch)
 
 
-def _put_vector(s, name, tensor, n, device):
+def _put_vector(s, name, tensor, n, device, dtype=None):
     if tensor is None:
         return
-    if not tensor.is_cuda or tensor.device != device or tensor.dtype != _torch().float32:
-        raise TypeError(f"{name} must be a float32 GPU tensor on the same device")
+    dtype = dtype or _torch().float32
+    if not tensor.is_cuda or tensor.device != device or tensor.dtype != dtype:
+        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} GPU tensor on the same device")
     if tuple(tensor.shape) != (n,) or not tensor.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
     setattr(s, name, tensor.data_ptr())
 
 
-def _linear(name, s, device, workspace, stream):
+def _linear(name, s, device, workspace, stream, operator="linear"):
     lib, ref = load(), ctypes.byref(s)
-    size = getattr(lib, f"dion_linear_{name}_workspace_size")
-    run = getattr(lib, f"dion_linear_{name}")
+    size = getattr(lib, f"dion_{operator}_{name}_workspace_size")
+    run = getattr(lib, f"dion_{operator}_{name}")
     return _launch(lambda: size(ref), lambda ws, nbytes, st: run(ref, ws, nbytes, st), device,
                    workspace, stream)
 
@@ -726,6 +745,54 @@ def linear_backward(dy, x=None, weight=None, dx=None, dw=None, db=None, act="non
     _put(s, "dw", "lddw", dw, (n, k), dy.dtype, dev)
     _put_vector(s, "db", db, n, dev)
     return _linear("backward", s, dev, workspace, stream)
+
+
+# --- cross entropy of an output head ---------------------------------------------
+
+def _xent(x, weight, target, ignore_index, label_smoothing, z_loss):
+    s = dion_cross_entropy(dtype=_linear_dtype(x, "x"), ignore_index=int(ignore_index),
+                           label_smoothing=float(label_smoothing), z_loss=float(z_loss))
+    if weight.dim() != 2:
+        raise ValueError("weight must be 2-D")
+    t, k = x.shape
+    n = weight.shape[0]
+    s.t, s.n, s.k = t, n, k
+    _put(s, "x", "ldx", x, (t, k), x.dtype, x.device)
+    _put(s, "w", "ldw", weight, (n, k), x.dtype, x.device)
+    _put_vector(s, "target", target, t, x.device, _torch().int64)
+    return s
+
+
+def cross_entropy_forward(x, weight, target, loss=None, lse=None, ignore_index: int = -100,
+                          label_smoothing: float = 0.0, z_loss: float = 0.0, workspace=None,
+                          stream=None):
+    """Softmax cross entropy of the logits x weight^T, which are not kept
+    (dion_cross_entropy_forward).
+
+    x (t x k), weight (n x k): float32 or bfloat16, one type; target (t) int64.
+    loss, lse (t) float32 receive each token's loss (0 where target is
+    ignore_index) and the logarithm of its sum of exponentials, which the
+    backward needs; either may be left out.  Returns the workspace."""
+    s = _xent(x, weight, target, ignore_index, label_smoothing, z_loss)
+    _put_vector(s, "loss", loss, s.t, x.device)
+    _put_vector(s, "lse", lse, s.t, x.device)
+    return _linear("forward", s, x.device, workspace, stream, "cross_entropy")
+
+
+def cross_entropy_backward(dloss, x, weight, target, lse, dx=None, dw=None, ignore_index: int = -100,
+                           label_smoothing: float = 0.0, z_loss: float = 0.0,
+                           accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of cross_entropy_forward (dion_cross_entropy_backward): dx (t x
+    k) and dw (n x k), of x's type, those of the two that are given, from the
+    losses' gradients dloss (t, float32) and the forward's lse.  accumulate: add
+    to dw.  Returns the workspace."""
+    s = _xent(x, weight, target, ignore_index, label_smoothing, z_loss)
+    s.accumulate = int(bool(accumulate))
+    _put_vector(s, "dloss", dloss, s.t, x.device)
+    _put_vector(s, "lse", lse, s.t, x.device)
+    _put(s, "dx", "lddx", dx, (s.t, s.k), x.dtype, x.device)
+    _put(s, "dw", "lddw", dw, (s.n, s.k), x.dtype, x.device)
+    return _linear("backward", s, x.device, workspace, stream, "cross_entropy")
 
 
 # --- AdamW step ---------------------------------------------------------------

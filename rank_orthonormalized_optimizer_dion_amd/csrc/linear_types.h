@@ -18,6 +18,7 @@ struct LinOut {
   int32_t act;             // DION_ACT_*
   int32_t dtype;           // of y, residual and z: 0 float32, 1 bfloat16
   int32_t accumulate;      // out += acc (y only, no bias / act / residual)
+  int32_t wide;            // the residual is float32 whatever dtype is
 };
 
 // C (M x N) = sum over `nseg` plane pairs of A B^T, reduction length K.
