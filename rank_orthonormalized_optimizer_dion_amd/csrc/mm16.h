@@ -92,7 +92,9 @@ struct Tile16 {
   uint32_t off[PER];   // byte offset of this lane's source cell at k0 = 0
   int64_t xoff, ld;
 
-  static __device__ __forceinline__ int swz(int row) { return MC ? 4 * (row & 3) + 2 * ((row >> 3) & 1) : (row >> 2) & 3; }
+  static __device__ __forceinline__ int swz(int row) {
+    return MC ? 4 * (row & 3) + 2 * ((row >> 3) & 1) : (0x78 >> (2 * ((row >> 2) & 3))) & 3;   // 0, 2, 3, 1
+  }
 
   __device__ __forceinline__ void init(int64_t ld_, int x0, int xn) {
     ld = ld_;
