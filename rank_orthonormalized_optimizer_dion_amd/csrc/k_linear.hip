@@ -95,9 +95,13 @@ __device__ __forceinline__ void lin_out(const LinOut& o, int row, int col, int l
   store8(o.y, row * o.ldy + col, o.dtype, aligned16(o.y, o.ldy, o.dtype), left, v);
 }
 
-template <int TILE, int ST, LinKind KIND, int ACT>
-__global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
-  using S = LinShape<TILE, ST, KIND>;
+// Two wavefronts per SIMD: with room for more registers per lane the compiler
+// keeps a small tile's accumulators in the half of them that only matrix
+// instructions read, and copies them there and back in every step (linear
+// backward, 1021 tokens of 773 -> 2051 in float32: 121 us, 134 with the copies).
+template <int TILE, LinKind KIND, int ACT>
+__global__ __launch_bounds__(2 * TILE, 2) void k_lin_mm(LinProduct p) {
+  using S = LinShape<TILE, KIND>;
   __shared__ u32x4 smem[S::LDS_CELLS];
   const Work16 work{p.full, p.tx * p.ty - p.full, p.slices, p.part, p.count};
   const Item16 it = item16(work, xcd_item(blockIdx.x, gridDim.x));
@@ -111,13 +115,7 @@ __global__ __launch_bounds__(2 * TILE) void k_lin_mm(LinProduct p) {
   typename S::B tb;
   ta.init(p.lda, r0, p.M);
   tb.init(p.ldb, c0, p.N);
-  const Pairs pairs = plane_pairs(p.nseg);
-  tile_product<S>(ta, tb, Planes16{p.a, p.b, p.sa, p.sb}, p.nseg,
-                  [pairs](int i, int& a, int& b) {
-                    a = (pairs.a >> (4 * i)) & 15;
-                    b = (pairs.b >> (4 * i)) & 15;
-                  },
-                  kbeg, kend, smem, acc);
+  lin_product_tile<S>(p, ta, tb, kbeg, kend, smem, acc);
   if (!join16<S>(work, it, smem, acc)) return;
   tile_runs<S, false>(
       acc, smem,
@@ -256,22 +254,22 @@ __global__ __launch_bounds__(256) void k_lin_rows(LinSkinny p) {
     }
 }
 
-template <int TILE, int ST, LinKind KIND, int ACT>
+template <int TILE, LinKind KIND, int ACT>
 hipError_t product(const LinProduct& p, hipStream_t st) {
-  k_lin_mm<TILE, ST, KIND, ACT><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p);
+  k_lin_mm<TILE, KIND, ACT><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p);
   return hipGetLastError();
 }
 
-template <int TILE, int ST>
+template <int TILE>
 hipError_t product(const LinProduct& p, LinKind kind, hipStream_t st) {
-  if (kind == kLinDx) return product<TILE, ST, kLinDx, DION_ACT_NONE>(p, st);
-  if (kind == kLinDw) return product<TILE, ST, kLinDw, DION_ACT_NONE>(p, st);
+  if (kind == kLinDx) return product<TILE, kLinDx, DION_ACT_NONE>(p, st);
+  if (kind == kLinDw) return product<TILE, kLinDw, DION_ACT_NONE>(p, st);
   switch (p.out.act) {
-    case DION_ACT_RELU: return product<TILE, ST, kLinForward, DION_ACT_RELU>(p, st);
-    case DION_ACT_RELU2: return product<TILE, ST, kLinForward, DION_ACT_RELU2>(p, st);
-    case DION_ACT_GELU: return product<TILE, ST, kLinForward, DION_ACT_GELU>(p, st);
-    case DION_ACT_SILU: return product<TILE, ST, kLinForward, DION_ACT_SILU>(p, st);
-    default: return product<TILE, ST, kLinForward, DION_ACT_NONE>(p, st);
+    case DION_ACT_RELU: return product<TILE, kLinForward, DION_ACT_RELU>(p, st);
+    case DION_ACT_RELU2: return product<TILE, kLinForward, DION_ACT_RELU2>(p, st);
+    case DION_ACT_GELU: return product<TILE, kLinForward, DION_ACT_GELU>(p, st);
+    case DION_ACT_SILU: return product<TILE, kLinForward, DION_ACT_SILU>(p, st);
+    default: return product<TILE, kLinForward, DION_ACT_NONE>(p, st);
   }
 }
 
@@ -291,8 +289,8 @@ hipError_t rows(const LinSkinny& p, bool vec, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_lin_product(const LinProduct& p, LinKind kind, int tile, hipStream_t st) {
-  if (tile == 256) return product<256, 4>(p, kind, st);
-  return p.items <= kTileSlots256 ? product<128, 8>(p, kind, st) : product<128, 4>(p, kind, st);
+  if (tile == 256) return product<256>(p, kind, st);
+  return product<128>(p, kind, st);
 }
 
 hipError_t launch_lin_packs(const LinPacks& p, hipStream_t st) {

@@ -205,16 +205,16 @@ struct NsRun {
   }
 };
 
-template <int PL, int TILE, int ST, bool BMC>
-using NsShape = Shape16<F16, TILE, TILE, TILE / 64, 2, ST, PL, false, BMC>;
+template <int PL, int TILE, bool BMC>
+using NsShape = Shape16<F16, TILE, TILE, TILE / 64, 2, PL, false, BMC>;
 
 // One tile of one of the three products.  Products that are symmetric
 // compute the tiles on and above the diagonal and write each one's
 // transpose too.
-template <int PL, int TILE, int ST, NsEpi EPI>
-__global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
+template <int PL, int TILE, NsEpi EPI>
+__global__ __launch_bounds__(2 * TILE, 2) void k_ns_mm(NsLaunch L) {
   constexpr bool SYM = EPI == kNsGram || EPI == kNsGramPoly || EPI == kNsPoly;
-  using S = NsShape<PL, TILE, ST, !SYM>;
+  using S = NsShape<PL, TILE, !SYM>;
   __shared__ u32x4 smem[S::LDS_CELLS];
   NsDesc d;
   NsClass c;
@@ -366,16 +366,16 @@ __global__ __launch_bounds__(2 * TILE) void k_ns_mm(NsLaunch L) {
   }
 }
 
-template <int PL, int TILE, int ST>
+template <int PL, int TILE>
 hipError_t product(const NsLaunch& L, int items, NsEpi epi, hipStream_t st) {
   const dim3 grid(items), block(2 * TILE);
   switch (epi) {
-    case kNsGram: k_ns_mm<PL, TILE, ST, kNsGram><<<grid, block, 0, st>>>(L); break;
-    case kNsGramPoly: k_ns_mm<PL, TILE, ST, kNsGramPoly><<<grid, block, 0, st>>>(L); break;
-    case kNsPoly: k_ns_mm<PL, TILE, ST, kNsPoly><<<grid, block, 0, st>>>(L); break;
-    case kNsApply: k_ns_mm<PL, TILE, ST, kNsApply><<<grid, block, 0, st>>>(L); break;
-    case kNsOut: k_ns_mm<PL, TILE, ST, kNsOut><<<grid, block, 0, st>>>(L); break;
-    case kNsStep: k_ns_mm<PL, TILE, ST, kNsStep><<<grid, block, 0, st>>>(L); break;
+    case kNsGram: k_ns_mm<PL, TILE, kNsGram><<<grid, block, 0, st>>>(L); break;
+    case kNsGramPoly: k_ns_mm<PL, TILE, kNsGramPoly><<<grid, block, 0, st>>>(L); break;
+    case kNsPoly: k_ns_mm<PL, TILE, kNsPoly><<<grid, block, 0, st>>>(L); break;
+    case kNsApply: k_ns_mm<PL, TILE, kNsApply><<<grid, block, 0, st>>>(L); break;
+    case kNsOut: k_ns_mm<PL, TILE, kNsOut><<<grid, block, 0, st>>>(L); break;
+    case kNsStep: k_ns_mm<PL, TILE, kNsStep><<<grid, block, 0, st>>>(L); break;
   }
   return hipGetLastError();
 }
@@ -407,9 +407,8 @@ hipError_t launch_ns_load(const NsLaunch& L, int planes, hipStream_t st) {
 }
 
 hipError_t launch_ns_product(const NsLaunch& L, int items, NsEpi epi, int planes, int tile, hipStream_t st) {
-  if (tile == 256) return planes == 2 ? product<2, 256, 4>(L, items, epi, st) : product<1, 256, 4>(L, items, epi, st);
-  if (items <= kTileSlots256) return planes == 2 ? product<2, 128, 8>(L, items, epi, st) : product<1, 128, 8>(L, items, epi, st);
-  return planes == 2 ? product<2, 128, 4>(L, items, epi, st) : product<1, 128, 4>(L, items, epi, st);
+  if (tile == 256) return planes == 2 ? product<2, 256>(L, items, epi, st) : product<1, 256>(L, items, epi, st);
+  return planes == 2 ? product<2, 128>(L, items, epi, st) : product<1, 128>(L, items, epi, st);
 }
 
 }  // namespace dion

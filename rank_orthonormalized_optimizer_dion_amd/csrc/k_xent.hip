@@ -212,9 +212,9 @@ __device__ __forceinline__ void dz_tile(typename S::Acc (&acc)[S::FM][S::FN], co
   });
 }
 
-template <int TILE, int ST, bool GRAD>
-__global__ __launch_bounds__(2 * TILE) void k_xent_mm(LinProduct p, XentEpi e) {
-  using S = LinShape<TILE, ST, kLinForward>;
+template <int TILE, bool GRAD>
+__global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e) {
+  using S = LinShape<TILE, kLinForward>;
   static_assert(S::TM == 64 && S::F == 16, "rows of a wavefront");
   __shared__ u32x4 smem[S::LDS_CELLS];
   const Work16 work{p.full, p.tx * p.ty - p.full, p.slices, p.part, p.count};
@@ -229,13 +229,7 @@ __global__ __launch_bounds__(2 * TILE) void k_xent_mm(LinProduct p, XentEpi e) {
   typename S::B tb;
   ta.init(p.lda, r0, p.M);
   tb.init(p.ldb, c0, p.N);
-  const Pairs pairs = plane_pairs(p.nseg);
-  tile_product<S>(ta, tb, Planes16{p.a, p.b, p.sa, p.sb}, p.nseg,
-                  [pairs](int i, int& a, int& b) {
-                    a = (pairs.a >> (4 * i)) & 15;
-                    b = (pairs.b >> (4 * i)) & 15;
-                  },
-                  kbeg, kend, smem, acc);
+  lin_product_tile<S>(p, ta, tb, kbeg, kend, smem, acc);
   if (!join16<S>(work, it, smem, acc)) return;
   const int wave = wave16();
   const int row0 = r0 + (wave / S::WN) * S::TM, col0 = c0 + (wave % S::WN) * S::TN;
@@ -430,18 +424,18 @@ hipError_t skinny(const LinSkinny& s, const XentEpi& e, bool grad, hipStream_t s
   return hipGetLastError();
 }
 
-template <int TILE, int ST>
+template <int TILE>
 hipError_t product(const LinProduct& p, const XentEpi& e, bool grad, hipStream_t st) {
-  if (grad) k_xent_mm<TILE, ST, true><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
-  else k_xent_mm<TILE, ST, false><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
+  if (grad) k_xent_mm<TILE, true><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
+  else k_xent_mm<TILE, false><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st) {
-  if (tile == 256) return product<256, 4>(p, e, grad, st);
-  return p.items <= kTileSlots256 ? product<128, 8>(p, e, grad, st) : product<128, 4>(p, e, grad, st);
+  if (tile == 256) return product<256>(p, e, grad, st);
+  return product<128>(p, e, grad, st);
 }
 
 hipError_t launch_xent_skinny(const LinSkinny& s, const XentEpi& e, bool grad, hipStream_t st) {

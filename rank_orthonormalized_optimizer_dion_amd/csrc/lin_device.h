@@ -76,8 +76,27 @@ __device__ __forceinline__ Pairs plane_pairs(int nseg) {
   return nseg == 6 ? Pairs{0x001021u, 0x010201u} : nseg == 2 ? Pairs{0x01u, 0u} : Pairs{0u, 0u};
 }
 
-template <int TILE, int ST, LinKind KIND>
-using LinShape = Shape16<B16, TILE, TILE, TILE / 64, 2, ST, 1, KIND == kLinDw, KIND != kLinForward>;
+// The sum over a product's plane pairs.  One pair has a loop of its own: half
+// of the scalar instructions between its matrix instructions.
+template <class S>
+__device__ __forceinline__ void lin_product_tile(const LinProduct& p, const typename S::A& ta, const typename S::B& tb,
+                                                 int kbeg, int kend, u32x4* smem, typename S::Acc (&acc)[S::FM][S::FN]) {
+  const Planes16 planes{p.a, p.b, p.sa, p.sb};
+  if (p.nseg == 1) {
+    tile_product<S>(ta, tb, planes, 1, [](int, int& a, int& b) { a = b = 0; }, kbeg, kend, smem, acc);
+    return;
+  }
+  const Pairs pairs = plane_pairs(p.nseg);
+  tile_product<S>(ta, tb, planes, p.nseg,
+                  [pairs](int i, int& a, int& b) {
+                    a = (pairs.a >> (4 * i)) & 15;
+                    b = (pairs.b >> (4 * i)) & 15;
+                  },
+                  kbeg, kend, smem, acc);
+}
+
+template <int TILE, LinKind KIND>
+using LinShape = Shape16<B16, TILE, TILE, TILE / 64, 2, 1, KIND == kLinDw, KIND != kLinForward>;
 
 // The first of several planes of x.  A finite x above bfloat16's largest
 // number would round to infinity and leave -infinity for the next plane; it

@@ -15,16 +15,18 @@
 // Tiles go from global memory straight to LDS (global_load_lds, 16 bytes per
 // lane), no registers and no conversion.  A wavefront's 64 lanes write 64
 // consecutive 16-byte cells, so a swizzle can only permute which cell of the
-// source each lane fetches.  64 banks serve 16 cells at a time; the
-// permutations let 16 consecutive lanes cover 16 different cells modulo 16:
-//   K-major: cell (x, c) of a row of 4 cells sits at 4 x + (c ^ (x / 4) % 4);
+// source each lane fetches.  A 128-bit read is served in groups of 16 lanes,
+// lanes 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31, and so for the upper
+// 32 (measured by pairs of lanes); the permutations let each group cover 16
+// different cells modulo 16 (64 banks):
+//   K-major: cell (x, c) of a row of 4 cells sits at 4 x + (c ^ s), s = 0, 2, 3,
+//     1 for x / 4 % 4 = 0 .. 3;
 //   x-major: cell (k, c), c = x / 8, sits at k CPR + (c ^ (4 (k % 4) + 2
 //     (k / 8 % 2))); ds_read_b64_tr_b16 transposes 4 k by 16 x blocks on the
 //     way out.
-// Counted (share of the LDS's working cycles lost to conflicts): x-major tiles
-// of one plane 1%, K-major tiles of two planes 2%; K-major tiles of one plane
-// 50% (a read takes four cells of 16 rows there, two of 32 rows with two
-// planes), and products with an x-major tile of two planes 33%.
+// Counted (share of the LDS's working cycles lost to conflicts): K-major tiles
+// none, x-major tiles of one plane 1%, products with an x-major tile of two
+// planes 33%.
 #pragma once
 #include <type_traits>
 
@@ -112,14 +114,34 @@ struct Tile16 {
     }
   }
 
-  // WHOLE: the stage lies inside the reduction.
-  template <bool WHOLE>
+  // WHOLE: the stage lies inside the reduction: scalar base, 32-bit lane
+  // offsets, no address arithmetic per lane.  ASM: one of the two tiles is
+  // x-major.  Before such a tile's transposing read the compiler waits for all
+  // loads that it knows to write LDS (vmcnt(0)), whichever stage they fill, so
+  // it is not told; arrive16 has the waits that are needed.  (Gradients of a
+  // head of 32000 on 8192 tokens, width 4096: 5.15 ms, known to the compiler
+  // 5.72; both tiles K-major, where it does not wait and spreads the loads
+  // between matrix instructions: 1.72 ms, known 1.70.)
+  template <bool WHOLE, bool ASM>
   __device__ __forceinline__ void issue(const uint16_t* p, int k0, int K, u32x4* lds) const {
     const char* base = reinterpret_cast<const char*>(p + xoff + (MC ? k0 * ld : static_cast<int64_t>(PL) * k0));
     const int wave = wave16();
-    if constexpr (WHOLE) {
+    if constexpr (WHOLE && ASM) {
+      static_assert(PER == 2, "two loads per thread and stage");
+      const uint64_t at = static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(base)));
+      const u32x4 rsrc = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu, 0xffffffffu, 0x00020000u};
+      const uint32_t to = uniform32(static_cast<int>((uintptr_t)(lptr<void>)(lds))) + wave * 1024;
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is a reserved register
+      // wait states: five from a vector instruction's write of a scalar register
+      // to a load that reads it, one from m0's write to the load into LDS
+      asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds\n\t"
+                   "s_mov_b32 m0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"v"(off[0]),
+                   "v"(off[PER - 1]), "s"(rsrc), "s"(to), "s"(to + NT * 16)
+                   : "memory", "m0");
+#pragma clang diagnostic pop
+    } else if constexpr (WHOLE) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass does not know the builtins' types
-      // scalar base, 32-bit lane offsets: no address arithmetic per lane
       const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_at(base)), 0, 0xffffffffu, 0x00020000);
 #pragma unroll
       for (int j = 0; j < PER; ++j)
@@ -165,11 +187,12 @@ struct Tile16 {
 
 // Shape of one tile product: BM x BN outputs, WM x WN wavefronts, ST LDS
 // stages (a power of two).
-template <class E_, int BM_, int BN_, int WM_, int WN_, int ST_, int PL_, bool AMC_, bool BMC_>
+template <class E_, int BM_, int BN_, int WM_, int WN_, int PL_, bool AMC_, bool BMC_>
 struct Shape16 {
   using E = E_;
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, PL = PL_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = 4, PL = PL_;
   static constexpr int NT = 64 * WM * WN;
+  static constexpr bool XMAJOR = AMC_ || BMC_;
   static constexpr int TM = BM / WM, TN = BN / WN;
   static constexpr int F = PL == 1 ? 16 : 32;            // side of a matrix instruction's output
   static constexpr int FM = TM / F, FN = TN / F;
@@ -255,10 +278,8 @@ __device__ __forceinline__ void interleave16() {
 // second it reads the first operands of stage t + 1 and starts the loads of
 // stage t + ST - 1.  So loads have ST - 2 steps to arrive, and a wavefront
 // always has a cluster whose operands are in registers when it reaches the
-// barrier.  Two wavefronts per SIMD (256 x 256 tiles, 4 stages) or two
-// workgroups per CU (128 x 128, 4 stages) fill each other's gaps; a launch
-// of too few 128 x 128 tiles for that takes 8 stages (against 4: the linear
-// layer from 3% faster to 2% slower, Newton-Schulz lists 1% to 3% slower).
+// barrier.  Two wavefronts per SIMD (256 x 256 tiles) or two workgroups per CU
+// (128 x 128) fill each other's gaps.
 // kend - kbeg is a multiple of a stage's k.
 template <class S, class Seg>
 __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typename S::B& tb,
@@ -270,8 +291,8 @@ __device__ __forceinline__ void tile_loop(const typename S::A& ta, const typenam
     int ia, ib;
     seg(is, ia, ib);
     u32x4* st = stage(t);
-    ta.template issue<true>(pl.a + ia * pl.sa, ik, kend, st);
-    tb.template issue<true>(pl.b + ib * pl.sb, ik, kend, st + S::A::CELLS);
+    ta.template issue<true, S::XMAJOR>(pl.a + ia * pl.sa, ik, kend, st);
+    tb.template issue<true, S::XMAJOR>(pl.b + ib * pl.sb, ik, kend, st + S::A::CELLS);
     ik += S::A::KS;
     const bool wrap = ik >= kend;
     ik = wrap ? kbeg : ik;
@@ -383,8 +404,8 @@ __device__ __forceinline__ void tile_product(const typename S::A& ta, const type
   for (int s = 0; kfull < kend && s < nseg; ++s) {
     int ia, ib;
     seg(s, ia, ib);
-    ta.template issue<false>(pl.a + ia * pl.sa, kfull, kend, smem);
-    tb.template issue<false>(pl.b + ib * pl.sb, kfull, kend, smem + S::A::CELLS);
+    ta.template issue<false, false>(pl.a + ia * pl.sa, kfull, kend, smem);
+    tb.template issue<false, false>(pl.b + ib * pl.sb, kfull, kend, smem + S::A::CELLS);
     arrive16<0>();
     Vec16<S> a[S::FM], b[S::FN];
     load_a<S>(a, smem, 0, 0);
