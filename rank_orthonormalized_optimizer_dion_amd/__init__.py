@@ -235,6 +235,11 @@ def _gdtype(G) -> int:
 def _stream_handle(stream, device) -> int:
     torch = _torch()
     if stream is None:
+        # the handle alone, where torch gives it: current_stream() builds an object
+        # for it, 2 us of a small call's 8
+        raw = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+        if raw is not None and device.index is not None:
+            return raw(device.index)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream)
 

@@ -3,6 +3,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "adamw_types.h"
 #include "dion.h"
@@ -50,7 +51,7 @@ int adamw_run(const dion_adamw_tensor* list, int count, double lr, double beta1,
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1) return DION_ERR_INVALID_ARG;
   if (!std::isfinite(lr) || !(eps >= 1.17549435e-38 && eps <= 1e30)) return DION_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(grad_scale) % 4 != 0) return DION_ERR_INVALID_ARG;
-  AdamwLaunch L{};
+  AdamwLaunch<kAdamwTensors> L{};
   // 1 - beta and the bias corrections are formed before they are rounded
   L.b1 = static_cast<float>(beta1);
   L.c1 = static_cast<float>(1.0 - beta1);
@@ -82,10 +83,10 @@ int adamw_run(const dion_adamw_tensor* list, int count, double lr, double beta1,
     const int64_t items = (a.n + adamw_chunk(quads) - 1) / adamw_chunk(quads);
     if (L.count == kAdamwTensors || items > INT32_MAX - L.total)
       if (flush() != hipSuccess) return DION_ERR_HIP;
-    AdamwTensor& t = L.t[L.count];
-    t = {a.X, a.G, a.M, a.V, a.S, a.n, static_cast<float>(1.0 - lr * a.weight_decay), 0};
     const int se = state_bits == DION_STATE_8BIT ? 4 : 16;   // bytes of four elements' states
-    t.vec = aligned(a.X, 16) && aligned(a.G, gdtype == DION_DTYPE_BF16 ? 8 : 16) && aligned(a.M, se) && aligned(a.V, se);
+    const bool vec = aligned(a.X, 16) && aligned(a.G, gdtype == DION_DTYPE_BF16 ? 8 : 16) && aligned(a.M, se) && aligned(a.V, se);
+    const AdamwTensor t = {a.X, a.G, a.M, a.V, a.S, 2 * a.n + vec, static_cast<float>(1.0 - lr * a.weight_decay)};
+    std::memcpy(L.t[L.count], &t, sizeof(L.t[0]));
     L.first[L.count++] = L.total;
     L.total += static_cast<int32_t>(items);
   }

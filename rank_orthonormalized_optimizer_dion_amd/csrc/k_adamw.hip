@@ -7,6 +7,7 @@
 // Every element is read and written once, in pieces of four per lane (16
 // bytes of float32).  With states in 8 bits, 16 lanes hold a block of 64
 // elements, whose largest magnitude they find among themselves.
+#include <cstddef>
 #include <type_traits>
 
 #include "adamw_types.h"
@@ -128,11 +129,11 @@ __device__ __forceinline__ void adamw_chunk_of(const AdamwTensor& t, int64_t bas
   GT gr[QUADS][4];
   ST ms[QUADS][4], vs[QUADS][4];
   uint32_t sm[QUADS], sv[QUADS];
-  const int64_t blocks = (t.n + kAdamwBlock - 1) / kAdamwBlock;
+  const int64_t blocks = (t.count() + kAdamwBlock - 1) / kAdamwBlock;
   const int64_t i0 = base + 4 * static_cast<int64_t>(threadIdx.x);
 #pragma unroll
   for (int q = 0; q < QUADS; ++q) {
-    const int64_t i = i0 + 1024 * q, left = t.n - i;
+    const int64_t i = i0 + 1024 * q, left = t.count() - i;
     load4<f32x4, VEC>(t.X, i, left, x[q]);
     load4<GV, VEC>(static_cast<const GT*>(t.G), i, left, gr[q]);
     load4<SV, VEC>(static_cast<const ST*>(t.M), i, left, ms[q]);
@@ -144,7 +145,7 @@ __device__ __forceinline__ void adamw_chunk_of(const AdamwTensor& t, int64_t bas
   }
 #pragma unroll
   for (int q = 0; q < QUADS; ++q) {
-    const int64_t i = i0 + 1024 * q, left = t.n - i;
+    const int64_t i = i0 + 1024 * q, left = t.count() - i;
     float m[4], v[4], r[4];
     if constexpr (BITS == 8) {
       uint32_t cm, cr;
@@ -218,49 +219,64 @@ __device__ __forceinline__ void adamw_chunk_of(const AdamwTensor& t, int64_t bas
 // The launch's arguments are read where they stand: a tensor's index is known
 // at run time only, and the arguments as a value indexed with it would be
 // copied to private memory first.
-template <bool BF, int BITS, int QUADS>
-__global__ __launch_bounds__(256) void k_adamw(AdamwLaunch arg) {
-  typedef __attribute__((address_space(4))) const AdamwLaunch* kptr;
+template <bool BF, int BITS, int QUADS, int CAP>
+__global__ __launch_bounds__(256) void k_adamw(AdamwLaunch<CAP> arg) {
+  typedef __attribute__((address_space(4))) const AdamwLaunch<CAP>* kptr;
   const kptr L = (kptr)__builtin_amdgcn_kernarg_segment_ptr();
   (void)arg;
-  const int item = blockIdx.x;
+  const int item = blockIdx.x, count = L->count;
   int which = 0;
-  if (L->count > 1) {
+  if constexpr (CAP > 4) {   // a lane looks at one tensor's first workgroup, or two
+    static_assert(CAP <= 128, "two tensors per lane");
     const int lane = threadIdx.x & 63;
-    const uint64_t past = __ballot(lane < L->count && L->first[lane] <= item);
-    which = __popcll(past) - 1;
-  }
-  typedef __attribute__((address_space(4))) const uint32_t* cptr;
-  const cptr src = (cptr)(&L->t[__builtin_amdgcn_readfirstlane(which)]);
-  struct { uint32_t w[sizeof(AdamwTensor) / 4]; } u;
+    which = __popcll(__ballot(lane < count && L->first[min(lane, CAP - 1)] <= item)) +
+            __popcll(__ballot(lane + 64 < count && L->first[min(lane + 64, CAP - 1)] <= item)) - 1;
+  } else {
 #pragma unroll
-  for (size_t k = 0; k < sizeof(AdamwTensor) / 4; ++k) u.w[k] = src[k];
-  const AdamwTensor t = __builtin_bit_cast(AdamwTensor, u);
-  const int64_t base = static_cast<int64_t>(item - L->first[__builtin_amdgcn_readfirstlane(which)]) * (1024 * QUADS);
+    for (int i = 1; i < CAP; ++i) which += i < count && L->first[i] <= item;
+  }
+  which = __builtin_amdgcn_readfirstlane(which);
+  struct { uint32_t w[kAdamwWords]; } u;
+#pragma unroll
+  for (int k = 0; k < kAdamwWords; ++k) u.w[k] = L->t[which][k];
+  AdamwTensor t;
+  __builtin_memcpy(&t, &u, sizeof(u));
+  const int64_t base = static_cast<int64_t>(item - L->first[which]) * (1024 * QUADS);
   float scale = 1.0f;
   if (L->grad_scale) {
     scale = *L->grad_scale;
     // not finite: the whole step leaves everything as it was
     if ((__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u) return;
   }
-  if (t.vec)
+  if (t.vec())
     adamw_chunk_of<BF, BITS, QUADS, true>(t, base, L->b1, L->c1, L->b2, L->c2, L->rate, L->root, L->eps, L->seed, scale);
   else
     adamw_chunk_of<BF, BITS, QUADS, false>(t, base, L->b1, L->c1, L->b2, L->c2, L->rate, L->root, L->eps, L->seed, scale);
 }
 
-template <bool BF, int BITS>
-hipError_t go(const AdamwLaunch& L, int quads, hipStream_t st) {
-  if (quads == 4) k_adamw<BF, BITS, 4><<<dim3(L.total), dim3(256), 0, st>>>(L);
-  else k_adamw<BF, BITS, 1><<<dim3(L.total), dim3(256), 0, st>>>(L);
+template <bool BF, int BITS, int CAP>
+hipError_t go(const AdamwLaunch<CAP>& L, int quads, hipStream_t st) {
+  if (quads == 4) k_adamw<BF, BITS, 4, CAP><<<dim3(L.total), dim3(256), 0, st>>>(L);
+  else k_adamw<BF, BITS, 1, CAP><<<dim3(L.total), dim3(256), 0, st>>>(L);
   return hipGetLastError();
+}
+template <int CAP>
+hipError_t go(const AdamwLaunch<CAP>& L, int gdtype, int state_bits, int quads, hipStream_t st) {
+  if (gdtype) return state_bits == 8 ? go<true, 8>(L, quads, st) : go<true, 32>(L, quads, st);
+  return state_bits == 8 ? go<false, 8>(L, quads, st) : go<false, 32>(L, quads, st);
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const AdamwLaunch& L, int gdtype, int state_bits, int quads, hipStream_t st) {
-  if (gdtype) return state_bits == 8 ? go<true, 8>(L, quads, st) : go<true, 32>(L, quads, st);
-  return state_bits == 8 ? go<false, 8>(L, quads, st) : go<false, 32>(L, quads, st);
+hipError_t launch_adamw(const AdamwLaunch<kAdamwTensors>& L, int gdtype, int state_bits, int quads, hipStream_t st) {
+  if (L.count > kAdamwFew) return go(L, gdtype, state_bits, quads, st);
+  AdamwLaunch<kAdamwFew> few;
+  __builtin_memcpy(&few, &L, offsetof(AdamwLaunch<kAdamwFew>, first));
+  for (int i = 0; i < kAdamwFew; ++i) {
+    few.first[i] = L.first[i];
+    __builtin_memcpy(few.t[i], L.t[i], sizeof(few.t[i]));
+  }
+  return go(few, gdtype, state_bits, quads, st);
 }
 
 }  // namespace dion

@@ -105,7 +105,7 @@ __device__ __forceinline__ float dz_of(float z, float lse, float a, float b, int
 // Eight values of dz (COUNT of them) as bfloat16 planes.
 template <int COUNT>
 __device__ __forceinline__ void store_dz(const XentEpi& e, int64_t row, int col, const float (&v)[COUNT]) {
-  uint16_t* at = e.dz + row * e.pitch + col;
+  uint16_t* at = e.dz + row * e.ld + col;
   float rest[COUNT];
   uint16_t h[COUNT];
   for (int pl = 0; pl < e.planes; ++pl) {
@@ -246,25 +246,34 @@ __global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e
   }
 }
 
-// Few tokens, bfloat16: 16 columns per workgroup, 16 lanes per token.
+// Few tokens, bfloat16: 16 columns per workgroup, 16 lanes per token.  What
+// the rows need is loaded before the products, not after them.
 template <int TB, bool GRAD>
 __global__ __launch_bounds__(512) void k_xent_skinny(LinSkinny p, XentEpi e) {
   __shared__ float red[8][TB][16][17];
+  constexpr int B = (TB + 1) / 2;   // 512 threads hold 32 tokens
   const int n0 = blockIdx.x * kXentGroup;
+  const int c = threadIdx.x & 15, col = n0 + c;
+  XentRow r[B];
+  int64_t y[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int token = 32 * b + (threadIdx.x >> 4);
+    if constexpr (GRAD) r[b] = xent_row(e, token, p.t, y[b]);
+    else y[b] = token < p.t ? e.target[token] : -1;
+  }
   skinny_sums<TB>(p, n0, red);
   __syncthreads();
 #pragma unroll
-  for (int b = 0; b < TB; b += 2) {   // 512 threads hold 32 tokens
-    const int token = 16 * b + (threadIdx.x >> 4), c = threadIdx.x & 15, col = n0 + c;
+  for (int b = 0; b < B; ++b) {
+    const int token = 32 * b + (threadIdx.x >> 4);
     if (token >= 16 * TB) continue;
     float z = 0.0f;
 #pragma unroll
     for (int s = 0; s < 8; ++s) z += red[s][token >> 4][token & 15][c];
     if constexpr (GRAD) {
-      int64_t y;
-      const XentRow r = xent_row(e, token, p.t, y);
-      float v[1] = {dz_of(z, r.lse, r.a, r.b, r.mask)};
-      if (y == e.j0 + col) v[0] -= r.c;
+      float v[1] = {dz_of(z, r[b].lse, r[b].a, r[b].b, r[b].mask)};
+      if (y[b] == e.j0 + col) v[0] -= r[b].c;
       if (col >= p.n) v[0] = 0.0f;
       if (token < p.t && col < e.pitch) store_dz<1>(e, token, col, v);
     } else {
@@ -272,7 +281,7 @@ __global__ __launch_bounds__(512) void k_xent_skinny(LinSkinny p, XentEpi e) {
       const float hi = row_max(in ? z : -INFINITY), base = base_of(hi);
       const float s = row_sum(in ? exp_fast(z - base) : 0.0f), total = e.total ? row_sum(in ? z : 0.0f) : 0.0f;
       if (token < p.t) {
-        if (in && e.target[token] == e.j0 + col) e.hit[token] = z;
+        if (in && y[b] == e.j0 + col) e.hit[token] = z;
         if (c == 0) {
           const int64_t at = static_cast<int64_t>(e.col0 + blockIdx.x) * p.t + token;
           e.top[at] = hi;

@@ -197,11 +197,16 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
   e.share = static_cast<float>(static_cast<double>(a.label_smoothing) / static_cast<double>(a.n));
   e.slope = 2.0f * a.z_loss;
   e.pitch = lin_cdiv(piece, 64) * 64;
-  e.plane = prows * e.pitch;
   e.planes = planes;
   e.prows = static_cast<int32_t>(path == kXentTiles ? prows : a.t);
-  e.dz = r.ws.take<uint16_t>(planes * e.plane);
-  const Operand dz{e.dz, e.pitch, e.plane};
+  // two planes lie row by row beside each other: dx then takes them as twice
+  // the rows, in one sweep over W, and adds each pair (24 tokens, 2048 -> 32000:
+  // dx 49 us, as two sweeps 77)
+  const bool fold = planes == 2;
+  e.ld = fold ? 2 * e.pitch : e.pitch;
+  e.plane = fold ? e.pitch : prows * e.pitch;
+  e.dz = r.ws.take<uint16_t>(planes * prows * e.pitch);
+  const Operand dz{e.dz, e.ld, e.plane}, dzrows{e.dz, e.pitch, 0};
   // dx over several pieces is summed in float32
   const bool sum = a.dx && piece < a.n && !f32;
   float* dxsum = sum ? r.ws.take<float>(a.t * a.k) : nullptr;
@@ -232,7 +237,9 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
         o.ldr = a.k;
         o.wide = 1;
       }
-      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, !lin_direct(c.w), nseg, kLinDx, o);
+      dx = fold ? lin_product(r, dzrows, w, 2 * a.t, a.k, wj.rows, !lin_direct(c.w), 1, kLinDx, o)
+                : lin_product(r, dz, w, a.t, a.k, wj.rows, !lin_direct(c.w), nseg, kLinDx, o);
+      dx.p.fold = fold;
     }
     if (a.dw) {
       LinOut o = out;

@@ -28,7 +28,8 @@ struct XentEpi {
   float keep, share;       // 1 - smoothing, smoothing / vocab
   float slope;             // 2 z-loss
   uint16_t* dz;
-  int64_t pitch, plane;
+  int64_t pitch;           // columns, padded
+  int64_t ld, plane;       // elements from row to row, from plane to plane
   int32_t prows, planes;
 };
 
