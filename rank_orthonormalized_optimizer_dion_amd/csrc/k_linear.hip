@@ -117,35 +117,15 @@ __global__ __launch_bounds__(2 * TILE, 2) void k_lin_mm(LinProduct p) {
   tb.init(p.ldb, c0, p.N);
   lin_product_tile<S>(p, ta, tb, kbeg, kend, smem, acc);
   if (!join16<S>(work, it, smem, acc)) return;
-  if constexpr (KIND == kLinDx) {
-    if (p.fold) {   // both planes of a row are in one lane
-#pragma unroll
-      for (int m = 0; m < S::FM; ++m)
-#pragma unroll
-        for (int n = 0; n < S::FN; ++n) {
-          acc[m][n][0] += acc[m][n][1];
-          acc[m][n][2] += acc[m][n][3];
-        }
-    }
-  }
-  const int M = KIND == kLinDx && p.fold ? p.M / 2 : p.M;
-  // the output row of a tile's row, or none
-  const auto row_of = [&](int r) {
-    const int row = r0 + r;
-    if constexpr (KIND == kLinDx) {
-      if (p.fold) return row & 1 ? M : row >> 1;
-    }
-    return row;
-  };
   tile_runs<S, false>(
       acc, smem,
       [&](int r, int q) {
-        const int row = row_of(r), col = c0 + q;
-        return row < M && col < p.N ? lin_fetch(p.out, row, col, p.N - col) : LinPre{};
+        const int row = r0 + r, col = c0 + q;
+        return row < p.M && col < p.N ? lin_fetch(p.out, row, col, p.N - col) : LinPre{};
       },
       [&](int r, int q, const float (&v)[8], const LinPre& pre) {
-        const int row = row_of(r), col = c0 + q;
-        if (row < M && col < p.N) lin_out<ACT>(p.out, row, col, p.N - col, v, pre);
+        const int row = r0 + r, col = c0 + q;
+        if (row < p.M && col < p.N) lin_out<ACT>(p.out, row, col, p.N - col, v, pre);
       });
 }
 

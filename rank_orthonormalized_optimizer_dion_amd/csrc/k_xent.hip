@@ -17,50 +17,11 @@
 #include "dion.h"
 #include "lin_device.h"
 #include "work16.h"
-#include "xent_types.h"
+#include "xent_device.h"
 
 namespace dion {
 
 namespace {
-
-constexpr float kLog2E = 1.44269504088896341f;
-
-// exp(x), one ulp of exp2 and x's rounding; x - y is formed first, so that the
-// largest term is exactly 1.
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
-
-// Lanes 16 r .. 16 r + 15 together (one DPP row).
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
-}
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
-}
-// quad_perm lane ^ 1, lane ^ 2, row_half_mirror, row_mirror
-__device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, dpp<0xb1>(v));
-  v = fmaxf(v, dpp<0x4e>(v));
-  v = fmaxf(v, dpp<0x141>(v));
-  return fmaxf(v, dpp<0x140>(v));
-}
-__device__ __forceinline__ float row_sum(float v) {
-  v += dpp<0xb1>(v);
-  v += dpp<0x4e>(v);
-  v += dpp<0x141>(v);
-  return v + dpp<0x140>(v);
-}
-
-// A largest value as what is subtracted: nothing where there is no value.
-__device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }
-
-// (top, sum) of two sets of logits together.
-__device__ __forceinline__ void merge(float& top, float& sum, float t2, float s2) {
-  const float t = fmaxf(top, t2), b = base_of(t);
-  sum = sum * exp_fast(top - b) + s2 * exp_fast(t2 - b);
-  top = t;
-}
 
 // f(integral_constant 0), f(1), ...: DPP controls have to be constants.
 template <class F, int... I>
@@ -72,51 +33,19 @@ __device__ __forceinline__ void each(F f) {
   each(f, std::make_integer_sequence<int, N>{});
 }
 
-// What dz needs of a row.  Rows without loss, and rows past the last, have
-// `mask` zero: their dz is zero whatever their logits are.  A target outside
-// the vocabulary makes its row NaN.
-struct XentRow {
-  float lse, a, b, c;
-  int mask;
-};
-__device__ __forceinline__ XentRow xent_row(const XentEpi& e, int row, int t, int64_t& y) {
-  XentRow r{0.0f, 0.0f, 0.0f, 0.0f, 0};
-  y = -1;
-  if (row < t) {
-    const int64_t target = e.target[row];
-    if (target != e.ignore) {
-      const bool in = target >= 0 && target < e.vocab;
-      const float d = in ? e.dloss[row] : NAN;
-      y = in ? target : -1;
-      r.lse = e.lse[row];
-      r.a = d * (1.0f + e.slope * r.lse);
-      r.b = d * e.share;
-      r.c = d * e.keep;
-      r.mask = -1;
-    }
-  }
-  return r;
-}
-__device__ __forceinline__ float dz_of(float z, float lse, float a, float b, int mask) {
-  const float d = a * exp_fast(z - lse) - b;
-  return __uint_as_float(__float_as_uint(d) & mask);
-}
-
-// Eight values of dz (COUNT of them) as bfloat16 planes.
-template <int COUNT>
-__device__ __forceinline__ void store_dz(const XentEpi& e, int64_t row, int col, const float (&v)[COUNT]) {
-  uint16_t* at = e.dz + row * e.ld + col;
-  float rest[COUNT];
-  uint16_t h[COUNT];
+// Eight values of dz as bfloat16 planes.
+__device__ __forceinline__ void store_dz(const XentEpi& e, int64_t row, int col, const float (&v)[8]) {
+  uint16_t* at = e.dz + row * e.pitch + col;
+  float rest[8];
+  uint16_t h[8];
   for (int pl = 0; pl < e.planes; ++pl) {
 #pragma unroll
-    for (int k = 0; k < COUNT; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const float x = pinned(pl == 0 ? v[k] : rest[k]);
       h[k] = pl == 0 && e.planes > 1 ? first_plane(x) : to_bf16(x);
       rest[k] = x - bf16_to_f32(h[k]);
     }
-    if constexpr (COUNT == 8) *reinterpret_cast<u32x4*>(at + pl * e.plane) = pack8(h);
-    else at[pl * e.plane] = h[0];
+    *reinterpret_cast<u32x4*>(at + pl * e.plane) = pack8(h);
   }
 }
 
@@ -239,122 +168,10 @@ __global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e
         acc, smem, [](int, int) { return NoPre{}; },
         [&](int r, int q, const float (&v)[8], const NoPre&) {
           const int row = r0 + r, col = c0 + q;
-          if (row < e.prows && col < e.pitch) store_dz<8>(e, row, col, v);
+          if (row < e.prows && col < e.pitch) store_dz(e, row, col, v);
         });
   } else {
     stats_tile<S>(acc, e, p.M, p.N, row0, col0, e.col0 + 2 * tj + wave % S::WN);
-  }
-}
-
-// Few tokens, bfloat16: 16 columns per workgroup, 16 lanes per token.  What
-// the rows need is loaded before the products, not after them.
-template <int TB, bool GRAD>
-__global__ __launch_bounds__(512) void k_xent_skinny(LinSkinny p, XentEpi e) {
-  __shared__ float red[8][TB][16][17];
-  constexpr int B = (TB + 1) / 2;   // 512 threads hold 32 tokens
-  const int n0 = blockIdx.x * kXentGroup;
-  const int c = threadIdx.x & 15, col = n0 + c;
-  XentRow r[B];
-  int64_t y[B];
-#pragma unroll
-  for (int b = 0; b < B; ++b) {
-    const int token = 32 * b + (threadIdx.x >> 4);
-    if constexpr (GRAD) r[b] = xent_row(e, token, p.t, y[b]);
-    else y[b] = token < p.t ? e.target[token] : -1;
-  }
-  skinny_sums<TB>(p, n0, red);
-  __syncthreads();
-#pragma unroll
-  for (int b = 0; b < B; ++b) {
-    const int token = 32 * b + (threadIdx.x >> 4);
-    if (token >= 16 * TB) continue;
-    float z = 0.0f;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) z += red[s][token >> 4][token & 15][c];
-    if constexpr (GRAD) {
-      float v[1] = {dz_of(z, r[b].lse, r[b].a, r[b].b, r[b].mask)};
-      if (y[b] == e.j0 + col) v[0] -= r[b].c;
-      if (col >= p.n) v[0] = 0.0f;
-      if (token < p.t && col < e.pitch) store_dz<1>(e, token, col, v);
-    } else {
-      const bool in = col < p.n;
-      const float hi = row_max(in ? z : -INFINITY), base = base_of(hi);
-      const float s = row_sum(in ? exp_fast(z - base) : 0.0f), total = e.total ? row_sum(in ? z : 0.0f) : 0.0f;
-      if (token < p.t) {
-        if (in && y[b] == e.j0 + col) e.hit[token] = z;
-        if (c == 0) {
-          const int64_t at = static_cast<int64_t>(e.col0 + blockIdx.x) * p.t + token;
-          e.top[at] = hi;
-          e.sum[at] = s;
-          if (e.total) e.total[at] = total;
-        }
-      }
-    }
-  }
-}
-
-// Few tokens in float32 or of any alignment: 4 columns per wavefront.
-template <int T, bool BF, bool VEC, bool GRAD>
-__global__ __launch_bounds__(256) void k_xent_rows(LinSkinny p, XentEpi e) {
-  __shared__ float part[3][4][T];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * kXentGroup + 4 * wave;
-  float z[4][T];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) row_sums<T, BF, VEC>(p, min(n0 + c, p.n - 1), z[c]);
-  if constexpr (GRAD) {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-      if (lane == i && i < p.t) {
-        int64_t y;
-        const XentRow r = xent_row(e, i, p.t, y);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = n0 + c;
-          float v[1] = {dz_of(z[c][i], r.lse, r.a, r.b, r.mask)};
-          if (y == e.j0 + col) v[0] -= r.c;
-          if (col >= p.n) v[0] = 0.0f;
-          if (col < e.pitch) store_dz<1>(e, i, col, v);
-        }
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      float hi = -INFINITY, s = 0.0f, total = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (n0 + c < p.n) hi = fmaxf(hi, z[c][i]);
-      const float base = base_of(hi);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (n0 + c < p.n) {
-          s += exp_fast(z[c][i] - base);
-          total += z[c][i];
-        }
-      if (lane == i && i < p.t) {
-        part[0][wave][i] = hi;
-        part[1][wave][i] = s;
-        part[2][wave][i] = total;
-        const int64_t y = e.target[i] - e.j0 - n0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (y == c && n0 + c < p.n) e.hit[i] = z[c][i];
-      }
-    }
-    __syncthreads();
-    const int i = threadIdx.x;
-    if (i < T && i < p.t) {
-      float hi = part[0][0][i], s = part[1][0][i], total = part[2][0][i];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        merge(hi, s, part[0][w][i], part[1][w][i]);
-        total += part[2][w][i];
-      }
-      const int64_t at = static_cast<int64_t>(e.col0 + blockIdx.x) * p.t + i;
-      e.top[at] = hi;
-      e.sum[at] = s;
-      if (e.total) e.total[at] = total;
-    }
   }
 }
 
@@ -408,31 +225,6 @@ __global__ __launch_bounds__(256) void k_xent_join(XentJoin j) {
   j.loss[row] = loss;
 }
 
-template <int T, bool BF, bool GRAD>
-hipError_t rows(const LinSkinny& s, const XentEpi& e, bool vec, int groups, hipStream_t st) {
-  if (vec) k_xent_rows<T, BF, true, GRAD><<<dim3(groups), dim3(256), 0, st>>>(s, e);
-  else k_xent_rows<T, BF, false, GRAD><<<dim3(groups), dim3(256), 0, st>>>(s, e);
-  return hipGetLastError();
-}
-template <int T>
-hipError_t rows(const LinSkinny& s, const XentEpi& e, bool grad, bool vec, int groups, hipStream_t st) {
-  if (s.out.dtype) return grad ? rows<T, true, true>(s, e, vec, groups, st) : rows<T, true, false>(s, e, vec, groups, st);
-  return grad ? rows<T, false, true>(s, e, vec, groups, st) : rows<T, false, false>(s, e, vec, groups, st);
-}
-
-// Workgroups of 16 columns: those of the piece, or of dz's padded rows.
-int groups_of(const LinSkinny& s, const XentEpi& e, bool grad) {
-  return grad ? static_cast<int>(e.pitch / kXentGroup) : (s.n + kXentGroup - 1) / kXentGroup;
-}
-
-template <int TB>
-hipError_t skinny(const LinSkinny& s, const XentEpi& e, bool grad, hipStream_t st) {
-  const dim3 grid(groups_of(s, e, grad)), block(512);
-  if (grad) k_xent_skinny<TB, true><<<grid, block, 0, st>>>(s, e);
-  else k_xent_skinny<TB, false><<<grid, block, 0, st>>>(s, e);
-  return hipGetLastError();
-}
-
 template <int TILE>
 hipError_t product(const LinProduct& p, const XentEpi& e, bool grad, hipStream_t st) {
   if (grad) k_xent_mm<TILE, true><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
@@ -445,17 +237,6 @@ hipError_t product(const LinProduct& p, const XentEpi& e, bool grad, hipStream_t
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st) {
   if (tile == 256) return product<256>(p, e, grad, st);
   return product<128>(p, e, grad, st);
-}
-
-hipError_t launch_xent_skinny(const LinSkinny& s, const XentEpi& e, bool grad, hipStream_t st) {
-  if (s.t <= 16) return skinny<1>(s, e, grad, st);
-  return s.t <= 32 ? skinny<2>(s, e, grad, st) : skinny<4>(s, e, grad, st);
-}
-
-hipError_t launch_xent_rows(const LinSkinny& s, const XentEpi& e, bool grad, bool vec, hipStream_t st) {
-  const int groups = groups_of(s, e, grad);
-  if (s.t == 1) return rows<1>(s, e, grad, vec, groups, st);
-  return s.t <= 4 ? rows<4>(s, e, grad, vec, groups, st) : rows<8>(s, e, grad, vec, groups, st);
 }
 
 hipError_t launch_xent_join(const XentJoin& j, hipStream_t st) {

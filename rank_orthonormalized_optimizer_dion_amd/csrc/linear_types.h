@@ -33,7 +33,6 @@ struct LinProduct {
   int32_t full, slices;       // mm16.h, Work16
   float* part;
   uint32_t* count;
-  int32_t fold;               // dx: rows 2 r and 2 r + 1 of A are the two planes of output row r
   LinOut out;
 };
 

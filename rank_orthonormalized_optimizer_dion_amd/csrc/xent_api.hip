@@ -82,23 +82,8 @@ int64_t xent_piece(int64_t n, int64_t row) {
   return std::min(n, std::max(kXentStep, kXentPiece / row / kXentStep * kXentStep));
 }
 
-// How z is computed: rows and skinny products of few tokens, or tiles.
-enum XentPath { kXentRows, kXentSkinny, kXentTiles };
-XentPath xent_path(const XentCall& c, bool& vec) {
-  const dion_cross_entropy& a = c.a;
-  const int64_t v = 16 / c.e;
-  vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldx % v == 0 &&
-        a.ldw % v == 0 && a.k % v == 0;
-  if (lin_direct(c.x) && lin_direct(c.w) && a.t <= kSkinnyTokens) return kXentSkinny;
-  return a.t <= kRowTokens ? kXentRows : kXentTiles;
-}
-
-LinSkinny xent_skinny(const XentCall& c, const Span& w) {
-  LinSkinny s{c.a.x, w.p, c.a.ldx, w.ld, static_cast<int32_t>(c.a.t), static_cast<int32_t>(w.rows),
-              static_cast<int32_t>(c.a.k), {}};
-  s.out.dtype = c.e == 2;
-  return s;
-}
+// Few tokens: their own kernels (k_xent_few.hip).
+bool xent_few(const XentCall& c) { return c.a.t <= (c.e == 2 ? kXentFewBf16 : kXentFewF32); }
 
 // The products of one piece or call, after the copies that they need; the
 // copies and counters of the launch are then done.
@@ -115,17 +100,57 @@ struct XentRun : Run {
   }
 };
 
+XentFew few_args(const XentCall& c, const Span& w) {
+  XentFew f{};
+  f.w = w.p;
+  f.ldw = w.ld;
+  f.n = static_cast<int32_t>(w.rows);
+  f.k = static_cast<int32_t>(c.a.k);
+  f.t = static_cast<int32_t>(c.a.t);
+  f.tp = c.a.t <= 32 ? 32 : c.a.t <= 64 ? 64 : 128;
+  return f;
+}
+
+// x's planes (and its transpose's) for the kernels of few tokens; a bfloat16 x
+// of whole 16-byte pieces is used as it is.
+hipError_t few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed, XentFew& f) {
+  const int64_t P = c.e == 2 ? 1 : 3;
+  XentPrep a{c.a.x, c.a.ldx, f.t, f.k, f.tp, nullptr, 0, 0, nullptr, 0};
+  f.x = c.a.x;
+  f.ldx = c.a.ldx;
+  f.kx = f.k;
+  if (planes && !lin_direct(c.x)) {
+    a.ldp = lin_cdiv(f.k, 64) * 64;
+    a.xplane = f.t * a.ldp;
+    a.xp = r.ws.take<uint16_t>(P * a.xplane);
+    f.x = a.xp;
+    f.ldx = a.ldp;
+    f.xplane = a.xplane;
+    f.kx = static_cast<int32_t>(a.ldp);
+  }
+  if (transposed) {
+    a.xtplane = static_cast<int64_t>(f.k) * f.tp;
+    a.xt = r.ws.take<uint16_t>(P * a.xtplane);
+    f.xt = a.xt;
+    f.xtplane = a.xtplane;
+  }
+  return r.go && (a.xp || a.xt) ? launch_few_prep(a, c.e == 4, r.st) : hipSuccess;
+}
+
+// Workgroups of z's kernel: up to four per CU, which then take several blocks
+// of 16 rows in turn.
+int64_t few_groups(int64_t n) { return std::min<int64_t>(lin_cdiv(n, kXentGroup), 1024); }
+
 hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const dion_cross_entropy& a = c.a;
   if (a.t == 0) return hipSuccess;
-  bool vec;
-  const XentPath path = xent_path(c, vec);
+  const bool few = xent_few(c);
   const int planes = c.e == 2 ? 1 : 3;
   // a piece at a time only where W has to be copied
-  const bool copy = path == kXentTiles && !lin_direct(c.w);
+  const bool copy = !few && !lin_direct(c.w);
   const int64_t piece = copy ? xent_piece(a.n, 2 * planes * lin_cdiv(a.k, 64) * 64) : a.n;
   // one partial column per 64 columns at least
-  const int64_t most = path == kXentTiles ? lin_cdiv(a.n, 64) + 2 * lin_cdiv(a.n, piece) : xent_group_cols(a.n);
+  const int64_t most = few ? few_groups(a.n) : lin_cdiv(a.n, 64) + 2 * lin_cdiv(a.n, piece);
   XentEpi e{};
   e.target = a.target;
   e.ignore = a.ignore_index;
@@ -135,12 +160,12 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   if (a.label_smoothing > 0.0f) e.total = r.ws.take<float>(most * a.t);
   e.hit = r.ws.take<float>(a.t);
   int64_t cols = 0;
-  if (path != kXentTiles) {
-    cols = xent_group_cols(a.n);
-    if (r.go) {
-      const LinSkinny s = xent_skinny(c, c.w);
-      LIN_TRY(path == kXentSkinny ? launch_xent_skinny(s, e, false, r.st) : launch_xent_rows(s, e, false, vec, r.st));
-    }
+  if (few) {
+    cols = most;
+    XentFew f = few_args(c, c.w);
+    const bool raw = a.t <= 16 && !lin_direct(c.x);
+    LIN_TRY(few_prep(r, c, !raw, false, f));
+    if (r.go) LIN_TRY(launch_few_z(f, e, c.e == 4, false, raw, static_cast<int>(cols), r.st));
   } else {
     Operand x;
     lin_operand(r, c.x, x);
@@ -166,27 +191,8 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   return launch_xent_join(j, r.st);
 }
 
-hipError_t xent_backward(XentRun& r, const XentCall& c) {
+XentEpi xent_grad(const XentCall& c, int planes, int64_t rows, int64_t piece) {
   const dion_cross_entropy& a = c.a;
-  if (!a.dx && !a.dw) return hipSuccess;
-  bool vec;
-  const XentPath path = xent_path(c, vec);
-  const bool f32 = c.e == 4;
-  const int planes = f32 ? 3 : a.t <= kLinFewTokens ? 2 : 1;
-  const int nseg = f32 ? 6 : planes;
-  LinOut out{};
-  out.dtype = !f32;
-  if (a.t == 0) {   // no tokens: dW is zero
-    if (!a.dw || a.accumulate) return hipSuccess;
-    out.y = a.dw;
-    out.ldy = a.lddw;
-    const Product dw = lin_product(r, Operand{}, Operand{}, a.n, a.k, 0, false, 1, kLinDw, out);
-    LIN_TRY(r.packs());
-    return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
-  }
-  const int64_t prows = lin_cdiv(a.t, kLinStage) * kLinStage;
-  const int64_t wcopy = lin_direct(c.w) ? 0 : 2 * (f32 ? 3 : 1) * lin_cdiv(a.k, 64) * 64;
-  const int64_t piece = xent_piece(a.n, std::max(2 * planes * prows, wcopy));
   XentEpi e{};
   e.target = a.target;
   e.ignore = a.ignore_index;
@@ -197,31 +203,85 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
   e.share = static_cast<float>(static_cast<double>(a.label_smoothing) / static_cast<double>(a.n));
   e.slope = 2.0f * a.z_loss;
   e.pitch = lin_cdiv(piece, 64) * 64;
+  e.plane = rows * e.pitch;
   e.planes = planes;
-  e.prows = static_cast<int32_t>(path == kXentTiles ? prows : a.t);
-  // two planes lie row by row beside each other: dx then takes them as twice
-  // the rows, in one sweep over W, and adds each pair (24 tokens, 2048 -> 32000:
-  // dx 49 us, as two sweeps 77)
-  const bool fold = planes == 2;
-  e.ld = fold ? 2 * e.pitch : e.pitch;
-  e.plane = fold ? e.pitch : prows * e.pitch;
-  e.dz = r.ws.take<uint16_t>(planes * prows * e.pitch);
-  const Operand dz{e.dz, e.ld, e.plane}, dzrows{e.dz, e.pitch, 0};
+  e.prows = static_cast<int32_t>(rows);
+  return e;
+}
+
+hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
+  const dion_cross_entropy& a = c.a;
+  const bool f32 = c.e == 4;
+  const int planes = f32 ? 3 : 2;
+  XentFew f = few_args(c, c.w);
+  const int64_t piece = xent_piece(a.n, 2 * planes * (a.t + f.tp));
+  XentEpi e = xent_grad(c, planes, a.t, piece);
+  LIN_TRY(few_prep(r, c, true, a.dw != nullptr, f));
+  e.dz = r.ws.take<uint16_t>(planes * e.plane);
+  f.dztplane = e.pitch * f.tp;
+  f.dzt = r.ws.take<uint16_t>(planes * f.dztplane);
+  // dx: about four workgroups per CU over the columns and the rows of W
+  const int64_t pieces = lin_cdiv(a.n, piece), across = lin_cdiv(a.k, f32 ? 64 : 128);
+  const int64_t parts = std::max<int64_t>(1, std::min(lin_cdiv(1024, across), lin_cdiv(piece, 128)));
+  float* part = a.dx ? r.ws.take<float>(pieces * parts * a.t * a.k) : nullptr;
+  if (!r.go) return hipSuccess;
+  for (int64_t p = 0; p < pieces; ++p) {
+    const int64_t j0 = p * piece;
+    const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
+    f.w = wj.p;
+    f.n = static_cast<int32_t>(wj.rows);
+    e.j0 = static_cast<int32_t>(j0);
+    LIN_TRY(launch_few_z(f, e, f32, true, false, static_cast<int>(few_groups(e.pitch)), r.st));
+    if (a.dx) LIN_TRY(launch_few_dx(f, e, f32, static_cast<int>(parts), part + p * parts * a.t * a.k, r.st));
+    if (a.dw) {
+      const Span dj = xent_rows(c.dw, j0, wj.rows);
+      // about four workgroups per CU again, in whole steps of 64 columns
+      const int64_t down = lin_cdiv(wj.rows, 4 * kFewDwRows);
+      const int64_t split = std::min(lin_cdiv(a.k, 64), lin_cdiv(1024, down));
+      const XentDw d{const_cast<void*>(dj.p), a.lddw, static_cast<int32_t>(lin_cdiv(lin_cdiv(a.k, split), 64) * 64), a.accumulate};
+      LIN_TRY(launch_few_dw(f, d, f32, r.st));
+    }
+  }
+  return a.dx ? launch_few_dxsum(f, part, static_cast<int>(pieces * parts), a.dx, a.lddx, !f32, r.st) : hipSuccess;
+}
+
+hipError_t xent_backward(XentRun& r, const XentCall& c) {
+  const dion_cross_entropy& a = c.a;
+  if (!a.dx && !a.dw) return hipSuccess;
+  const bool f32 = c.e == 4;
+  LinOut out{};
+  out.dtype = !f32;
+  if (a.t == 0) {   // no tokens: dW is zero
+    if (!a.dw || a.accumulate) return hipSuccess;
+    out.y = a.dw;
+    out.ldy = a.lddw;
+    const Product dw = lin_product(r, Operand{}, Operand{}, a.n, a.k, 0, false, 1, kLinDw, out);
+    LIN_TRY(r.packs());
+    return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
+  }
+  if (xent_few(c)) return xent_backward_few(r, c);
+  const int planes = f32 ? 3 : 1, nseg = f32 ? 6 : 1;
+  const int64_t prows = lin_cdiv(a.t, kLinStage) * kLinStage;
+  const int64_t wcopy = lin_direct(c.w) ? 0 : 2 * planes * lin_cdiv(a.k, 64) * 64;
+  const int64_t piece = xent_piece(a.n, std::max(2 * planes * prows, wcopy));
+  XentEpi e = xent_grad(c, planes, prows, piece);
+  e.dz = r.ws.take<uint16_t>(planes * e.plane);
+  const Operand dz{e.dz, e.pitch, e.plane};
   // dx over several pieces is summed in float32
   const bool sum = a.dx && piece < a.n && !f32;
   float* dxsum = sum ? r.ws.take<float>(a.t * a.k) : nullptr;
   Operand x{};
-  if (path == kXentTiles || a.dw) lin_operand(r, c.x, x);
+  lin_operand(r, c.x, x);
+  const bool padded = !lin_direct(c.w), xpadded = !lin_direct(c.x);
   const size_t mark = r.ws.used;
   for (int64_t j0 = 0; j0 < a.n; j0 += piece) {
     r.ws.used = mark;
     const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
     const bool last = j0 + piece >= a.n;
     Operand w{};
-    if (path == kXentTiles || a.dx) lin_operand(r, wj, w);
-    Product z{}, dx{}, dw{};
-    if (path == kXentTiles)
-      z = lin_product(r, x, w, a.t, wj.rows, a.k, !lin_direct(c.x) && !lin_direct(c.w), f32 ? 6 : 1, kLinForward, LinOut{});
+    lin_operand(r, wj, w);
+    Product dx{}, dw{};
+    const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, padded && xpadded, nseg, kLinForward, LinOut{});
     if (a.dx) {
       LinOut o = out;
       o.y = a.dx;
@@ -237,9 +297,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
         o.ldr = a.k;
         o.wide = 1;
       }
-      dx = fold ? lin_product(r, dzrows, w, 2 * a.t, a.k, wj.rows, !lin_direct(c.w), 1, kLinDx, o)
-                : lin_product(r, dz, w, a.t, a.k, wj.rows, !lin_direct(c.w), nseg, kLinDx, o);
-      dx.p.fold = fold;
+      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, padded, nseg, kLinDx, o);
     }
     if (a.dw) {
       LinOut o = out;
@@ -247,17 +305,12 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
       o.y = const_cast<void*>(dj.p);
       o.ldy = a.lddw;
       o.accumulate = a.accumulate != 0;
-      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, path == kXentTiles && !lin_direct(c.x), nseg, kLinDw, o);
+      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, xpadded, nseg, kLinDw, o);
     }
     e.j0 = static_cast<int32_t>(j0);
     LIN_TRY(r.packs());
     if (r.go) {
-      if (path == kXentTiles) {
-        LIN_TRY(launch_xent_product(z.p, e, true, z.tile, r.st));
-      } else {
-        const LinSkinny s = xent_skinny(c, wj);
-        LIN_TRY(path == kXentSkinny ? launch_xent_skinny(s, e, true, r.st) : launch_xent_rows(s, e, true, vec, r.st));
-      }
+      LIN_TRY(launch_xent_product(z.p, e, true, z.tile, r.st));
       if (a.dx) LIN_TRY(launch_lin_product(dx.p, kLinDx, dx.tile, r.st));
       if (a.dw) LIN_TRY(launch_lin_product(dw.p, kLinDw, dw.tile, r.st));
     }

@@ -28,8 +28,7 @@ struct XentEpi {
   float keep, share;       // 1 - smoothing, smoothing / vocab
   float slope;             // 2 z-loss
   uint16_t* dz;
-  int64_t pitch;           // columns, padded
-  int64_t ld, plane;       // elements from row to row, from plane to plane
+  int64_t pitch, plane;    // elements from row to row, from plane to plane
   int32_t prows, planes;
 };
 
@@ -46,16 +45,52 @@ struct XentJoin {
   float keep, smoothing, z_loss;
 };
 
-// Partial columns of a piece of n columns.
-constexpr int kXentGroup = 16;   // columns of a workgroup with few tokens
+// Partial columns of a launch of tiles.
 inline int64_t xent_tile_cols(int64_t ty) { return 2 * ty; }   // two wavefronts across a tile
-inline int64_t xent_group_cols(int64_t n) { return (n + kXentGroup - 1) / kXentGroup; }
 
-// z by tiles, by the matrix cores for up to 64 tokens, by rows for up to 8
-// (s.out: dtype of x and W only); grad: backward.
+// Few tokens (k_xent_few.hip).
+constexpr int kXentFewBf16 = 64, kXentFewF32 = 128;   // tokens
+constexpr int kXentGroup = 16;     // rows of W that a workgroup turns into z at a time
+constexpr int kFewDwRows = 64;     // rows of dW of a wavefront (half of it beyond 64 tokens)
+struct XentFew {
+  const void* w;           // n rows of k
+  int64_t ldw;
+  int32_t n, k, t;
+  const void* x;           // t rows: planes in bfloat16, 16-byte aligned, or x itself
+  int64_t ldx, xplane;
+  int32_t kx;              // columns that are there (and zero from k on)
+  int32_t tp;              // tokens of the transposed operands: t up to 32, 64 or 128
+  const uint16_t* xt;      // planes of k x tp
+  int64_t xtplane;
+  uint16_t* dzt;           // planes of pitch x tp
+  int64_t dztplane;
+};
+struct XentPrep {
+  const void* x;
+  int64_t ldx;
+  int32_t t, k, tp;
+  uint16_t* xp;            // planes of t x ldp, zero past k; or null
+  int64_t ldp, xplane;
+  uint16_t* xt;            // or null
+  int64_t xtplane;
+};
+struct XentDw {
+  void* dw;
+  int64_t ld;
+  int32_t cols;            // of a workgroup
+  int32_t accumulate;
+};
+// raw: x as it is (at most 16 tokens, no grad); groups: workgroups, each of
+// which leaves one partial column
+hipError_t launch_few_z(const XentFew& f, const XentEpi& e, bool f32, bool grad, bool raw, int groups, hipStream_t st);
+hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st);
+hipError_t launch_few_dx(const XentFew& f, const XentEpi& e, bool f32, int parts, float* part, hipStream_t st);
+hipError_t launch_few_dxsum(const XentFew& f, const float* part, int parts, void* dx, int64_t lddx, int dtype,
+                            hipStream_t st);
+hipError_t launch_few_dw(const XentFew& f, const XentDw& d, bool f32, hipStream_t st);
+
+// z by tiles; grad: backward.
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st);
-hipError_t launch_xent_skinny(const LinSkinny& s, const XentEpi& e, bool grad, hipStream_t st);
-hipError_t launch_xent_rows(const LinSkinny& s, const XentEpi& e, bool grad, bool vec, hipStream_t st);
 hipError_t launch_xent_join(const XentJoin& j, hipStream_t st);
 
 }  // namespace dion
