@@ -66,7 +66,7 @@ __device__ __forceinline__ LinPre lin_fetch(const LinOut& o, int row, int col, i
   const void* src = o.accumulate ? o.y : o.residual;
   const int64_t ld = o.accumulate ? o.ldy : o.ldr;
   const int dtype = o.wide ? 0 : o.dtype;
-  if (src) load8(src, row * ld + col, dtype, aligned16(src, ld, dtype), left, p.w);
+  if (src) load8(src, row * ld + col, dtype, left, p.w);
   return p;
 }
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ void lin_out(const LinOut& o, int row, int col, int l
     for (int k = 0; k < 8; ++k)
       if (k < left) v[k] += o.bias[col + k];
   }
-  if (o.z) store8(o.z, row * o.ldz + col, o.dtype, aligned16(o.z, o.ldz, o.dtype), left, v);
+  if (o.z) store8(o.z, row * o.ldz + col, o.dtype, left, v);
   if (act != DION_ACT_NONE) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], act);
@@ -92,7 +92,7 @@ __device__ __forceinline__ void lin_out(const LinOut& o, int row, int col, int l
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += pre.w[k];
   }
-  store8(o.y, row * o.ldy + col, o.dtype, aligned16(o.y, o.ldy, o.dtype), left, v);
+  store8(o.y, row * o.ldy + col, o.dtype, left, v);
 }
 
 // Two wavefronts per SIMD: with room for more registers per lane the compiler
@@ -138,17 +138,16 @@ __device__ __forceinline__ void pack_block(const LinPack& p, int block, float (&
   const int lane = threadIdx.x >> 5;
   const int64_t r0 = static_cast<int64_t>(by) * p.chunk;
   const int64_t r1 = min(p.prows, r0 + p.chunk);
-  const bool vs = aligned16(p.src, p.ld, p.dtype), vz = aligned16(p.z, p.ldz, p.dtype);
   const int left = p.cols - col;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (col < (p.dst ? p.pitch : p.cols)) {
     for (int64_t r = r0 + lane; r < r1; r += 8) {
       const int in = r < p.rows ? left : 0;   // rows past the last are zero
       float v[8];
-      load8(p.src, r * p.ld + col, p.dtype, vs, in, v);
+      load8(p.src, r * p.ld + col, p.dtype, in, v);
       if (p.z) {
         float z[8];
-        load8(p.z, r * p.ldz + col, p.dtype, vz, in, z);
+        load8(p.z, r * p.ldz + col, p.dtype, in, z);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= k < in ? act_slope(z[k], p.act) : 0.0f;
       }

@@ -1,4 +1,4 @@
-// Cross entropy of few tokens (up to 64 in bfloat16, 128 in float32): reading
+// Cross entropy of few tokens (up to 64): reading
 // W once per product, and writing dW, is what it costs, in any type and at any
 // alignment.  All products run on the bfloat16 matrix cores with operands that
 // come straight from global memory into registers:
@@ -80,50 +80,128 @@ __device__ __forceinline__ f32x4 mfma_planes(const Planes8<PA>& a, const Planes8
   }
 }
 
-// Sixteen consecutive elements from column c of a row of k, as two operands;
-// elements past the row are zero.  TAIL: the row may end inside.
+// What a lane reads of 64 consecutive elements of a row of k, from column c
+// (a multiple of 64): two operands of eight, elements 32 h + 8 g .. of the
+// lane's group g = lane / 16, so that every load takes 64 consecutive bytes of
+// a row.  In float32 an operand takes two loads, elements 32 h + 4 g .. and 32 h +
+// 16 + 4 g ..: x's planes are stored in that order (k_few_prep).  Elements past
+// the row are zero.  TAIL: the row may end inside.
+template <bool F32>
+struct Raw16 {
+  u32x4 v[F32 ? 4 : 2];
+};
 template <bool F32, bool TAIL>
-__device__ __forceinline__ void load16(const void* row, int c, int k, Planes8<F32 ? 3 : 1> (&o)[2]) {
+__device__ __forceinline__ Raw16<F32> load16(const void* row, int c, int k) {
+  constexpr int N = F32 ? 4 : 8;   // elements of a load
+  using T = typename std::conditional<F32, float, uint16_t>::type;
+  const int g = (threadIdx.x & 63) >> 4;
+  Raw16<F32> o;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c0 = c + 8 * h;
-    if constexpr (F32) {
-      const float* p = static_cast<const float*>(row) + c0;
-      float v[8];
-      if (!TAIL || c0 + 8 <= k) {
-        const f32x4 lo = load_any<f32x4>(p), hi = load_any<f32x4>(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = lo[i];
-          v[4 + i] = hi[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + i < k ? p[i] : 0.0f;
-      }
-      o[h] = split8(v);
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    const int c0 = c + (F32 ? 16 : 32) * i + N * g;
+    const T* p = static_cast<const T*>(row) + c0;
+    if (!TAIL || c0 + N <= k) {
+      o.v[i] = load_any<u32x4>(p);
     } else {
-      const uint16_t* p = static_cast<const uint16_t*>(row) + c0;
-      if (!TAIL || c0 + 8 <= k) {
-        o[h].p[0] = load_any<u32x4>(p);
-      } else {
-        uint16_t v[8];
+      T v[N];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + i < k ? p[i] : 0;
-        o[h].p[0] = pack8(v);
+      for (int j = 0; j < N; ++j) v[j] = c0 + j < k ? p[j] : T(0);
+      __builtin_memcpy(&o.v[i], v, 16);
+    }
+  }
+  return o;
+}
+template <bool F32>
+__device__ __forceinline__ Planes8<F32 ? 3 : 1> planes16(const Raw16<F32>& r, int h) {
+  if constexpr (F32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(r.v[2 * h][i]);
+      v[4 + i] = __uint_as_float(r.v[2 * h + 1][i]);
+    }
+    return split8(v);
+  } else {
+    return {{r.v[h]}};
+  }
+}
+
+// Pieces of z's reduction that a wavefront loads at a time.
+template <int TB, int RT, bool F32>
+constexpr int kFewZPieces = F32 ? (TB * RT == 1 ? 2 : 1) : TB * RT == 2 ? 4 : TB * RT <= 8 ? 2 : 1;
+
+// Planes of x (zero past its columns) and of its transpose (tokens padded by
+// zeros to a.tp), 64 columns per block.
+template <bool F32>
+__device__ __forceinline__ void prep_block(const XentPrep& a, int block, float* tile) {
+  constexpr int P = F32 ? 3 : 1;
+  const int c0 = block * 64, pitch = a.tp + 1;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < a.tp * 64; i += 512) {
+    const int token = i >> 6, c = i & 63;
+    const bool in = token < a.t && c0 + c < a.k;
+    float v = in ? load_value(a.x, token * a.ldx + c0 + c, !F32) : 0.0f;
+    tile[c * pitch + token] = v;
+    if (a.xp && token < a.t) {
+      // float32: the order of load16
+      const int at = F32 ? (c & ~31) + 8 * ((c & 15) >> 2) + (c & 3) + 4 * ((c >> 4) & 1) : c;
+      for (int pl = 0; pl < P; ++pl) {
+        const float u = pinned(v);
+        const uint16_t h = pl == 0 && P > 1 ? first_plane(u) : to_bf16(u);
+        v = u - bf16_to_f32(h);
+        a.xp[pl * a.xplane + token * a.ldp + c0 + at] = h;
       }
+    }
+  }
+  if (!a.xt) return;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < a.tp * 64; i += 512) {
+    const int token = i & (a.tp - 1), c = i / a.tp;
+    if (c0 + c >= a.k) continue;
+    float v = tile[c * pitch + token];
+    for (int pl = 0; pl < P; ++pl) {
+      const float u = pinned(v);
+      const uint16_t h = pl == 0 && P > 1 ? first_plane(u) : to_bf16(u);
+      v = u - bf16_to_f32(h);
+      a.xt[pl * a.xtplane + static_cast<int64_t>(c0 + c) * a.tp + token] = h;
     }
   }
 }
 
-// z for 16 rows of W at a time, its statistics or dz.  RAW: x is read as it
-// is, like W (one block of 16 tokens), else from planes whose rows are
-// readable, and zero past k, up to f.kx columns.
-template <int TB, bool F32, bool RAW, bool GRAD>
-__global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e) {
+template <bool F32>
+__global__ __launch_bounds__(512) void k_few_prep(XentPrep a) {
+  __shared__ float tile[64 * (kXentFew + 1)];
+  prep_block<F32>(a, blockIdx.x, tile);
+}
+
+// z for 16 RT rows of W at a time, its statistics or dz; the 8 wavefronts of a
+// workgroup take turns at 64-element pieces of the reduction.  What is read
+// again and again is x: RT blocks of rows share its operands (24 tokens, 2048
+// -> 32000 in bfloat16: @@).  RAW: x is read as it is, like W (one block of 16
+// tokens), else from planes whose rows are readable, and zero past k, up to f.kx
+// columns.  With dz, workgroups past the first `prep.first` transpose x for dW.
+template <int TB, int RT, bool F32, bool RAW, bool GRAD>
+__global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e, XentPrep prep) {
   constexpr int P = F32 ? 3 : 1, ES = F32 ? 4 : 2;
-  constexpr int B = (TB + 1) / 2;   // 512 threads hold 32 tokens by 16 columns
-  __shared__ float red[8][TB][16][17];
+  constexpr int B = (TB + 1) / 2;                       // 512 threads hold 32 tokens by 16 rows of W
+  constexpr int RR = RT * TB <= 8 ? RT : 8 / TB;   // blocks of rows that meet in LDS at a time
+  static_assert(RT % RR == 0, "whole rounds");
+  struct Sums {
+    float v[8][RR][TB][16][17];   // wavefront, block of rows, token / 16, token % 16, row
+  };
+  constexpr int kPrep = 64 * (16 * TB < 32 ? 33 : 16 * TB + 1);
+  __shared__ union {
+    Sums red;
+    float tile[GRAD ? kPrep : 1];
+  } lds;
+  if constexpr (GRAD) {
+    if (static_cast<int>(blockIdx.x) >= prep.first) {
+      prep_block<F32>(prep, blockIdx.x - prep.first, lds.tile);
+      return;
+    }
+  }
+  const int workers = GRAD ? prep.first : static_cast<int>(gridDim.x);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = threadIdx.x & 15;
   XentRow r[B];
@@ -141,81 +219,111 @@ __global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e) {
 #pragma unroll
   for (int b = 0; b < TB; ++b)
     xr[b] = static_cast<const char*>(f.x) + min(16 * b + (lane & 15), f.t - 1) * f.ldx * (RAW ? ES : 2);
-  const int groups = GRAD ? static_cast<int>(e.pitch / kXentGroup) : (f.n + kXentGroup - 1) / kXentGroup;
-  for (int g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int n0 = g * kXentGroup, col = n0 + c;
-    const char* wr = static_cast<const char*>(f.w) + min(n0 + (lane & 15), f.n - 1) * f.ldw * ES;
-    f32x4 acc[TB];
+  const int rows = GRAD ? static_cast<int>(e.pitch) : f.n;
+  for (int n0 = blockIdx.x * 16 * RT; n0 < rows; n0 += workers * 16 * RT) {
+    const char* wr[RT];
 #pragma unroll
-    for (int b = 0; b < TB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // 64 elements of the reduction: 16 per lane
-    const auto piece = [&](auto tail, int k0) {
+    for (int q = 0; q < RT; ++q)
+      wr[q] = static_cast<const char*>(f.w) + min(n0 + 16 * q + (lane & 15), f.n - 1) * f.ldw * ES;
+    f32x4 acc[RT][TB];
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int b = 0; b < TB; ++b) acc[q][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // U pieces of 64 elements of the reduction: W's loads, then the products
+    const auto pieces = [&](auto tail, auto count, int k0) {
       constexpr bool TAIL = decltype(tail)::value;
-      const int k = k0 + 16 * (lane >> 4);
-      Planes8<P> w[2], x[TB][2];
-      load16<F32, TAIL>(wr, k, f.k, w);
+      constexpr int N = decltype(count)::value;
+      Raw16<F32> w[N][RT], xw[N][RAW ? TB : 1];
+      Planes8<P> x[N][RAW ? 1 : TB][2];
 #pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        if constexpr (RAW) {
-          load16<F32, TAIL>(xr[b], k, f.k, x[b]);
-        } else {
+      for (int u = 0; u < N; ++u) {
+        const int k = k0 + 512 * u;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < RT; ++q) w[u][q] = load16<F32, TAIL>(wr[q], k, f.k);
 #pragma unroll
-            for (int pl = 0; pl < P; ++pl)
-              x[b][h].p[pl] = !TAIL || k + 8 * h < f.kx
-                                  ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(xr[b]) + pl * f.xplane + k + 8 * h)
-                                  : u32x4{0, 0, 0, 0};
-        }
-      }
+        for (int b = 0; b < TB; ++b) {
+          if constexpr (RAW) {
+            xw[u][b] = load16<F32, TAIL>(xr[b], k, f.k);
+          } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int b = 0; b < TB; ++b) acc[b] = mfma_planes(w[h], x[b][h], acc[b]);
-    };
-    int k0 = 64 * wave;
-    constexpr int U = F32 || TB > 2 ? 2 : 4;   // pieces in flight
-#pragma unroll U
-    for (; k0 + 64 <= f.k; k0 += 64 * 8) piece(std::false_type{}, k0);
-    if (k0 < f.k) piece(std::true_type{}, k0);
-    // lane l, register i: row 4 (l / 16) + i of W, token l % 16
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][b][lane & 15][4 * (lane >> 4) + i] = acc[b][i];
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int token = 32 * b + (threadIdx.x >> 4);
-      float z = 0.0f;
-      if (token < 16 * TB) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s) z += red[s][token >> 4][token & 15][c];
-      }
-      if constexpr (GRAD) {
-        float v[1] = {dz_of(z, r[b].lse, r[b].a, r[b].b, r[b].mask)};
-        if (y[b] == e.j0 + col) v[0] -= r[b].c;
-        if (col >= f.n || token >= f.t) v[0] = 0.0f;
-        if (token < f.tp) {   // dz by rows, and transposed with its tokens padded by zeros
-          float rest = v[0];
-          for (int pl = 0; pl < e.planes; ++pl) {
-            const float u = pinned(rest);
-            const uint16_t h = pl == 0 ? first_plane(u) : to_bf16(u);
-            rest = u - bf16_to_f32(h);
-            if (token < f.t) e.dz[pl * e.plane + token * e.pitch + col] = h;
-            f.dzt[pl * f.dztplane + static_cast<int64_t>(col) * f.tp + token] = h;
+              for (int pl = 0; pl < P; ++pl) {
+                const int c8 = k + 32 * h + 8 * (lane >> 4);
+                x[u][b][h].p[pl] = !TAIL || c8 < f.kx
+                                       ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(xr[b]) + pl * f.xplane + c8)
+                                       : u32x4{0, 0, 0, 0};
+              }
           }
         }
-      } else {
-        const bool in = col < f.n && token < f.t;
-        const float hi = row_max(in ? z : -INFINITY), base = base_of(hi);
-        const float s = row_sum(in ? exp_fast(z - base) : 0.0f);
-        merge(top[b], sum[b], hi, s);
-        if (e.total) total[b] += row_sum(in ? z : 0.0f);
-        if (in && y[b] == e.j0 + col) e.hit[token] = z;
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < RT; ++q) {
+            const Planes8<P> a = planes16<F32>(w[u][q], h);
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+              if constexpr (RAW) acc[q][b] = mfma_planes(a, planes16<F32>(xw[u][b], h), acc[q][b]);
+              else acc[q][b] = mfma_planes(a, x[u][b][h], acc[q][b]);
+            }
+          }
+    };
+    constexpr int U = kFewZPieces<TB, RT, F32>;
+    using std::integral_constant;
+    int k0 = 64 * wave;
+    if constexpr (U > 1)
+      for (; k0 + 512 * (U - 1) + 64 <= f.k; k0 += 512 * U) pieces(std::false_type{}, integral_constant<int, U>{}, k0);
+    for (; k0 + 64 <= f.k; k0 += 512) pieces(std::false_type{}, integral_constant<int, 1>{}, k0);
+    if (k0 < f.k) pieces(std::true_type{}, integral_constant<int, 1>{}, k0);
+#pragma unroll
+    for (int q0 = 0; q0 < RT; q0 += RR) {
+      // lane l, register i: row 4 (l / 16) + i of W, token l % 16
+#pragma unroll
+      for (int q = 0; q < RR; ++q)
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lds.red.v[wave][q][b][lane & 15][4 * (lane >> 4) + i] = acc[q0 + q][b][i];
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int q = 0; q < RR; ++q) {
+          const int token = 32 * b + (threadIdx.x >> 4), col = n0 + 16 * (q0 + q) + c;
+          float z = 0.0f;
+          if (token < 16 * TB) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) z += lds.red.v[s][q][token >> 4][token & 15][c];
+          }
+          if constexpr (GRAD) {
+            float v = dz_of(z, r[b].lse, r[b].a, r[b].b, r[b].mask);
+            if (y[b] == e.j0 + col) v -= r[b].c;
+            if (col >= f.n || token >= f.t) v = 0.0f;
+            if (token < f.tp && col < e.pitch) {   // dz by rows, and transposed with its tokens padded by zeros
+              for (int pl = 0; pl < e.planes; ++pl) {
+                const float u = pinned(v);
+                const uint16_t h = pl == 0 ? first_plane(u) : to_bf16(u);
+                v = u - bf16_to_f32(h);
+                if (token < f.t) e.dz[pl * e.plane + token * e.pitch + col] = h;
+                f.dzt[pl * f.dztplane + static_cast<int64_t>(col) * f.tp + token] = h;
+              }
+            }
+          } else {
+            const bool in = col < f.n && token < f.t;
+            const float hi = row_max(in ? z : -INFINITY), base = base_of(hi);
+            const float s = row_sum(in ? exp_fast(z - base) : 0.0f);
+            merge(top[b], sum[b], hi, s);
+            if (e.total) total[b] += row_sum(in ? z : 0.0f);
+            if (in && y[b] == e.j0 + col) e.hit[token] = z;
+          }
+        }
+      __syncthreads();
     }
-    __syncthreads();
   }
   if constexpr (!GRAD) {
 #pragma unroll
@@ -231,46 +339,10 @@ __global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e) {
   }
 }
 
-// Planes of x (zero past its columns) and of its transpose (tokens padded by
-// zeros to f.tp), 64 columns per workgroup.
-template <bool F32>
-__global__ __launch_bounds__(256) void k_few_prep(XentPrep a) {
-  constexpr int P = F32 ? 3 : 1;
-  __shared__ float tile[64][129];
-  const int c0 = blockIdx.x * 64;
-  for (int i = threadIdx.x; i < a.tp * 64; i += 256) {
-    const int token = i >> 6, c = i & 63;
-    const bool in = token < a.t && c0 + c < a.k;
-    float v = in ? load_value(a.x, token * a.ldx + c0 + c, !F32) : 0.0f;
-    tile[c][token] = v;
-    if (a.xp && token < a.t) {
-      for (int pl = 0; pl < P; ++pl) {
-        const float u = pinned(v);
-        const uint16_t h = pl == 0 && P > 1 ? first_plane(u) : to_bf16(u);
-        v = u - bf16_to_f32(h);
-        a.xp[pl * a.xplane + token * a.ldp + c0 + c] = h;
-      }
-    }
-  }
-  if (!a.xt) return;
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.tp * 64; i += 256) {
-    const int token = i % a.tp, c = i / a.tp;
-    if (c0 + c >= a.k) continue;
-    float v = tile[c][token];
-    for (int pl = 0; pl < P; ++pl) {
-      const float u = pinned(v);
-      const uint16_t h = pl == 0 && P > 1 ? first_plane(u) : to_bf16(u);
-      v = u - bf16_to_f32(h);
-      a.xt[pl * a.xtplane + static_cast<int64_t>(c0 + c) * a.tp + token] = h;
-    }
-  }
-}
-
 // dx's sums over every `gridDim.y`-th block of 4 x 32 rows of W, for 16
 // times CW columns.
 template <int TB, bool F32>
-__global__ __launch_bounds__(256) void k_few_dx(XentFew f, const uint16_t* dz, int64_t pitch, int64_t plane, float* part) {
+__global__ __launch_bounds__(256, 2) void k_few_dx(XentFew f, const uint16_t* dz, int64_t pitch, int64_t plane, float* part) {
   constexpr int CW = F32 ? 4 : 8, PW = F32 ? 3 : 1, PZ = F32 ? 3 : 2;
   using T = typename std::conditional<F32, float, uint16_t>::type;
   __shared__ float red[2][CW * TB * 4][64];
@@ -366,24 +438,30 @@ __global__ __launch_bounds__(256) void k_few_dx(XentFew f, const uint16_t* dz, i
     }
 }
 
-// dx from the partial sums, in order.
-__global__ __launch_bounds__(256) void k_few_dxsum(const float* part, int parts, int t, int k, void* dx, int64_t lddx,
-                                                   int dtype) {
-  const int64_t size = static_cast<int64_t>(t) * k, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+// 256 elements of dx from the partial sums, in order.
+__device__ __forceinline__ void dxsum_block(const XentDxSum& a, int64_t block) {
+  const int64_t size = static_cast<int64_t>(a.t) * a.k, i = block * 256 + threadIdx.x;
   if (i >= size) return;
   float s = 0.0f;
 #pragma unroll 8
-  for (int p = 0; p < parts; ++p) s += part[p * size + i];
-  const int64_t row = i / k;
-  store_value(dx, row * lddx + (i - row * k), dtype, s);
+  for (int p = 0; p < a.parts; ++p) s += a.part[p * size + i];
+  const int64_t row = i / a.k;
+  store_value(a.dx, row * a.ld + (i - row * a.k), a.dtype, s);
 }
+__global__ __launch_bounds__(256) void k_few_dxsum(XentDxSum a) { dxsum_block(a, blockIdx.x); }
 
 // dW: a wavefront's 16 RJ rows by the columns of its part, 64 at a time.
+// Workgroups past the first d.tiles sum up dx.
 template <int TT, bool F32>
-__global__ __launch_bounds__(256) void k_few_dw(XentFew f, XentDw d) {
-  constexpr int PX = F32 ? 3 : 1, PZ = F32 ? 3 : 2, RJ = kFewDwRows / 16 / (TT == 4 ? 2 : 1);
+__global__ __launch_bounds__(256, 2) void k_few_dw(XentFew f, XentDw d, XentDxSum sum) {
+  constexpr int PX = F32 ? 3 : 1, PZ = F32 ? 3 : 2, RJ = kFewDwRows / 16;
+  if (static_cast<int>(blockIdx.x) >= d.tiles) {
+    dxsum_block(sum, blockIdx.x - d.tiles);
+    return;
+  }
+  const int down = blockIdx.x % d.down, across = blockIdx.x / d.down;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j0 = (blockIdx.x * 4 + wave) * 16 * RJ;
+  const int j0 = (down * 4 + wave) * 16 * RJ;
   if (j0 >= f.n) return;
   Planes8<PZ> z[RJ][TT];
 #pragma unroll
@@ -395,13 +473,13 @@ __global__ __launch_bounds__(256) void k_few_dw(XentFew f, XentDw d) {
         z[q][s].p[pl] = *reinterpret_cast<const u32x4*>(
             f.dzt + pl * f.dztplane + static_cast<int64_t>(min(j0 + 16 * q + (lane & 15), f.n - 1)) * f.tp + 32 * s + 8 * (lane >> 4));
   const int r = lane & 15;
-  for (int c0 = blockIdx.y * d.cols; c0 < min(f.k, (static_cast<int>(blockIdx.y) + 1) * d.cols); c0 += 64) {
+  for (int c0 = across * d.cols; c0 < min(f.k, (across + 1) * d.cols); c0 += 64) {
     f32x4 acc[4][RJ];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      // the operand's row r is column 16 (r / 4) + 4 m + r % 4: a lane's outputs
-      // are then 16 consecutive columns
-      const int64_t c = min(c0 + 16 * (r >> 2) + 4 * m + (r & 3), f.k - 1);
+      // which column the operand's row r is is free: four lanes' stores of 16
+      // bytes are made 64 consecutive bytes
+      const int64_t c = min(c0 + (F32 ? 16 * m + r : 32 * (m >> 1) + 8 * (r >> 2) + 4 * (m & 1) + (r & 3)), f.k - 1);
 #pragma unroll
       for (int q = 0; q < RJ; ++q) acc[m][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -414,57 +492,60 @@ __global__ __launch_bounds__(256) void k_few_dw(XentFew f, XentDw d) {
         for (int q = 0; q < RJ; ++q) acc[m][q] = mfma_planes(x, z[q][s], acc[m][q]);
       }
     }
-    const int c = c0 + 16 * (lane >> 4);
+    constexpr int N = F32 ? 4 : 8;   // outputs of a store
 #pragma unroll
     for (int q = 0; q < RJ; ++q) {
       const int j = j0 + 16 * q + r;
       if (j >= f.n) continue;
-      const int64_t at = j * d.ld + c;
-      float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = acc[i / 4][q][i % 4];
-      if (c + 16 <= f.k) {
-        if constexpr (F32) {
-          float* p = static_cast<float*>(d.dw) + at;
+      for (int i = 0; i < 16 / N; ++i) {
+        const int c = c0 + 4 * N * i + N * (lane >> 4);
+        const int64_t at = j * d.ld + c;
+        float v[N];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f32x4 u = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-            if (d.accumulate) u += load_any<f32x4>(p + 4 * i);
-            __builtin_memcpy(p + 4 * i, &u, 16);
+        for (int u = 0; u < N; ++u) v[u] = acc[i * (N / 4) + u / 4][q][u % 4];
+        if (c + N <= f.k) {
+          if constexpr (F32) {
+            float* p = static_cast<float*>(d.dw) + at;
+            f32x4 u = {v[0], v[1], v[2], v[3]};
+            if (d.accumulate) u += load_any<f32x4>(p);
+            __builtin_memcpy(p, &u, 16);
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(d.dw) + at;
+            uint16_t h[8], old[8];
+            if (d.accumulate) __builtin_memcpy(old, p, 16);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) h[u] = to_bf16(d.accumulate ? v[u] + bf16_to_f32(old[u]) : v[u]);
+            const u32x4 u = pack8(h);
+            __builtin_memcpy(p, &u, 16);
           }
         } else {
-          uint16_t* p = static_cast<uint16_t*>(d.dw) + at;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint16_t h[8], old[8];
-            if (d.accumulate) __builtin_memcpy(old, p + 8 * i, 16);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = to_bf16(d.accumulate ? v[8 * i + k] + bf16_to_f32(old[k]) : v[8 * i + k]);
-            const u32x4 u = pack8(h);
-            __builtin_memcpy(p + 8 * i, &u, 16);
-          }
+          for (int u = 0; u < N; ++u)
+            if (c + u < f.k) store_value(d.dw, at + u, !F32, d.accumulate ? v[u] + load_value(d.dw, at + u, !F32) : v[u]);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < f.k) store_value(d.dw, at + i, !F32, d.accumulate ? v[i] + load_value(d.dw, at + i, !F32) : v[i]);
       }
     }
   }
 }
 
-template <int TB, bool F32>
-hipError_t few_z(const XentFew& f, const XentEpi& e, bool grad, bool raw, int groups, hipStream_t st) {
-  const dim3 grid(groups), block(512);
+template <int TB, int RT, bool F32>
+hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int groups, hipStream_t st) {
+  const dim3 grid(grad ? prep.first + (prep.xt ? (f.k + 63) / 64 : 0) : groups), block(512);
   if (grad) {
-    k_few_z<TB, F32, false, true><<<grid, block, 0, st>>>(f, e);
+    k_few_z<TB, RT, F32, false, true><<<grid, block, 0, st>>>(f, e, prep);
   } else if constexpr (TB == 1) {
-    if (raw) k_few_z<TB, F32, true, false><<<grid, block, 0, st>>>(f, e);
-    else k_few_z<TB, F32, false, false><<<grid, block, 0, st>>>(f, e);
+    if (raw) k_few_z<TB, RT, F32, true, false><<<grid, block, 0, st>>>(f, e, prep);
+    else k_few_z<TB, RT, F32, false, false><<<grid, block, 0, st>>>(f, e, prep);
   } else {
-    k_few_z<TB, F32, false, false><<<grid, block, 0, st>>>(f, e);
+    k_few_z<TB, RT, F32, false, false><<<grid, block, 0, st>>>(f, e, prep);
   }
   return hipGetLastError();
+}
+template <int TB, bool F32>
+hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int rt, int groups, hipStream_t st) {
+  if (rt == 1) return few_z<TB, 1, F32>(f, e, prep, grad, raw, groups, st);
+  return few_z<TB, F32 && TB == 4 ? 2 : 4, F32>(f, e, prep, grad, raw, groups, st);
 }
 
 template <int TB, bool F32>
@@ -474,55 +555,66 @@ hipError_t few_dx(const XentFew& f, const XentEpi& e, int parts, float* part, hi
   return hipGetLastError();
 }
 
+unsigned dxsum_blocks(const XentDxSum& s) { return s.dx ? static_cast<unsigned>((static_cast<int64_t>(s.t) * s.k + 255) / 256) : 0; }
+
 template <int TT, bool F32>
-hipError_t few_dw(const XentFew& f, const XentDw& d, hipStream_t st) {
-  constexpr int rows = 4 * kFewDwRows / (TT == 4 ? 2 : 1);
-  k_few_dw<TT, F32><<<dim3((f.n + rows - 1) / rows, (f.k + d.cols - 1) / d.cols), dim3(256), 0, st>>>(f, d);
+hipError_t few_dw(const XentFew& f, XentDw d, const XentDxSum& sum, hipStream_t st) {
+  constexpr int rows = 4 * kFewDwRows;
+  d.down = (f.n + rows - 1) / rows;
+  d.tiles = d.down * ((f.k + d.cols - 1) / d.cols);
+  k_few_dw<TT, F32><<<dim3(d.tiles + dxsum_blocks(sum)), dim3(256), 0, st>>>(f, d, sum);
   return hipGetLastError();
 }
 
 }  // namespace
 
+int few_rows(int t, bool f32, int64_t n) {
+  // 64 rows of W per workgroup where that still makes one per CU: x is read a
+  // quarter as often (24 tokens, 2048 -> 32000: 36 us, 55 with 16 rows; one
+  // token, whose lanes read the same row of x: 34 us, 30 with 16)
+  const int rt = f32 && t > 32 ? 2 : 4;
+  return t > 4 && n >= 256 * 16 * rt ? rt : 1;
+}
+
 hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st) {
-  const dim3 grid((a.k + 63) / 64), block(256);
+  const dim3 grid((a.k + 63) / 64), block(512);
   if (f32) k_few_prep<true><<<grid, block, 0, st>>>(a);
   else k_few_prep<false><<<grid, block, 0, st>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_few_z(const XentFew& f, const XentEpi& e, bool f32, bool grad, bool raw, int groups, hipStream_t st) {
+hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool f32, bool grad, bool raw, int rt,
+                        int groups, hipStream_t st) {
   if (f32) {
-    if (f.t <= 16) return few_z<1, true>(f, e, grad, raw, groups, st);
-    if (f.t <= 32) return few_z<2, true>(f, e, grad, raw, groups, st);
-    return f.t <= 64 ? few_z<4, true>(f, e, grad, raw, groups, st) : few_z<8, true>(f, e, grad, raw, groups, st);
+    if (f.t <= 16) return few_z<1, true>(f, e, prep, grad, raw, rt, groups, st);
+    if (f.t <= 32) return few_z<2, true>(f, e, prep, grad, raw, rt, groups, st);
+    return few_z<4, true>(f, e, prep, grad, raw, rt, groups, st);
   }
-  if (f.t <= 16) return few_z<1, false>(f, e, grad, raw, groups, st);
-  return f.t <= 32 ? few_z<2, false>(f, e, grad, raw, groups, st) : few_z<4, false>(f, e, grad, raw, groups, st);
+  if (f.t <= 16) return few_z<1, false>(f, e, prep, grad, raw, rt, groups, st);
+  return f.t <= 32 ? few_z<2, false>(f, e, prep, grad, raw, rt, groups, st)
+                   : few_z<4, false>(f, e, prep, grad, raw, rt, groups, st);
 }
 
 hipError_t launch_few_dx(const XentFew& f, const XentEpi& e, bool f32, int parts, float* part, hipStream_t st) {
   if (f32) {
     if (f.t <= 16) return few_dx<1, true>(f, e, parts, part, st);
     if (f.t <= 32) return few_dx<2, true>(f, e, parts, part, st);
-    return f.t <= 64 ? few_dx<4, true>(f, e, parts, part, st) : few_dx<8, true>(f, e, parts, part, st);
+    return few_dx<4, true>(f, e, parts, part, st);
   }
   if (f.t <= 16) return few_dx<1, false>(f, e, parts, part, st);
   return f.t <= 32 ? few_dx<2, false>(f, e, parts, part, st) : few_dx<4, false>(f, e, parts, part, st);
 }
 
-hipError_t launch_few_dxsum(const XentFew& f, const float* part, int parts, void* dx, int64_t lddx, int dtype,
-                            hipStream_t st) {
-  const int64_t size = static_cast<int64_t>(f.t) * f.k;
-  k_few_dxsum<<<dim3(static_cast<unsigned>((size + 255) / 256)), dim3(256), 0, st>>>(part, parts, f.t, f.k, dx, lddx, dtype);
+hipError_t launch_few_dxsum(const XentDxSum& s, hipStream_t st) {
+  k_few_dxsum<<<dim3(dxsum_blocks(s)), dim3(256), 0, st>>>(s);
   return hipGetLastError();
 }
 
-hipError_t launch_few_dw(const XentFew& f, const XentDw& d, bool f32, hipStream_t st) {
+hipError_t launch_few_dw(const XentFew& f, const XentDw& d, const XentDxSum& sum, bool f32, hipStream_t st) {
   if (f32) {
-    if (f.tp <= 32) return few_dw<1, true>(f, d, st);
-    return f.tp <= 64 ? few_dw<2, true>(f, d, st) : few_dw<4, true>(f, d, st);
+    return f.tp <= 32 ? few_dw<1, true>(f, d, sum, st) : few_dw<2, true>(f, d, sum, st);
   }
-  return f.tp <= 32 ? few_dw<1, false>(f, d, st) : few_dw<2, false>(f, d, st);
+  return f.tp <= 32 ? few_dw<1, false>(f, d, sum, st) : few_dw<2, false>(f, d, sum, st);
 }
 
 }  // namespace dion

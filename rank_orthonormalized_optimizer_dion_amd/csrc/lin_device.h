@@ -17,22 +17,22 @@ __device__ __forceinline__ void store_value(void* p, int64_t o, int dtype, float
   else static_cast<float*>(p)[o] = v;
 }
 
-// Eight consecutive values, as vectors where the address allows.
-__device__ __forceinline__ bool aligned16(const void* p, int64_t ld, int dtype) {
-  return (reinterpret_cast<uint64_t>(p) & 15) == 0 && ld % (dtype ? 8 : 4) == 0;
-}
-__device__ __forceinline__ void load8(const void* p, int64_t o, int dtype, bool vec, int left, float (&v)[8]) {
-  if (vec && left >= 8) {
+// Eight consecutive values, `left` of which exist, as vectors where all do:
+// global memory takes vector accesses at any address.
+__device__ __forceinline__ void load8(const void* p, int64_t o, int dtype, int left, float (&v)[8]) {
+  if (left >= 8) {
     if (dtype) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + o);
+      u32x4 u;
+      __builtin_memcpy(&u, static_cast<const uint16_t*>(p) + o, 16);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[2 * k] = __uint_as_float(u[k] << 16);
         v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
       }
     } else {
-      const float* q = static_cast<const float*>(p) + o;
-      const f32x4 a = *reinterpret_cast<const f32x4*>(q), b = *reinterpret_cast<const f32x4*>(q + 4);
+      f32x4 a, b;
+      __builtin_memcpy(&a, static_cast<const float*>(p) + o, 16);
+      __builtin_memcpy(&b, static_cast<const float*>(p) + o + 4, 16);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[k] = a[k];
@@ -44,17 +44,18 @@ __device__ __forceinline__ void load8(const void* p, int64_t o, int dtype, bool 
     for (int k = 0; k < 8; ++k) v[k] = k < left ? load_value(p, o + k, dtype) : 0.0f;
   }
 }
-__device__ __forceinline__ void store8(void* p, int64_t o, int dtype, bool vec, int left, const float (&v)[8]) {
-  if (vec && left >= 8) {
+__device__ __forceinline__ void store8(void* p, int64_t o, int dtype, int left, const float (&v)[8]) {
+  if (left >= 8) {
     if (dtype) {
       uint16_t h[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[k] = to_bf16(v[k]);
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + o) = pack8(h);
+      const u32x4 u = pack8(h);
+      __builtin_memcpy(static_cast<uint16_t*>(p) + o, &u, 16);
     } else {
-      float* q = static_cast<float*>(p) + o;
-      *reinterpret_cast<f32x4*>(q) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+      __builtin_memcpy(static_cast<float*>(p) + o, &a, 16);
+      __builtin_memcpy(static_cast<float*>(p) + o + 4, &b, 16);
     }
   } else {
 #pragma unroll

@@ -83,7 +83,9 @@ int64_t xent_piece(int64_t n, int64_t row) {
 }
 
 // Few tokens: their own kernels (k_xent_few.hip).
-bool xent_few(const XentCall& c) { return c.a.t <= (c.e == 2 ? kXentFewBf16 : kXentFewF32); }
+bool xent_few(const XentCall& c) {
+  return c.a.t <= (lin_direct(c.x) && lin_direct(c.w) ? kXentFewDirect : kXentFew);
+}
 
 // The products of one piece or call, after the copies that they need; the
 // copies and counters of the launch are then done.
@@ -107,15 +109,15 @@ XentFew few_args(const XentCall& c, const Span& w) {
   f.n = static_cast<int32_t>(w.rows);
   f.k = static_cast<int32_t>(c.a.k);
   f.t = static_cast<int32_t>(c.a.t);
-  f.tp = c.a.t <= 32 ? 32 : c.a.t <= 64 ? 64 : 128;
+  f.tp = c.a.t <= 32 ? 32 : 64;
   return f;
 }
 
-// x's planes (and its transpose's) for the kernels of few tokens; a bfloat16 x
-// of whole 16-byte pieces is used as it is.
-hipError_t few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed, XentFew& f) {
+// x's planes for the kernels of few tokens (a bfloat16 x of whole 16-byte
+// pieces is used as it is), and where its transpose's go.
+XentPrep few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed, XentFew& f) {
   const int64_t P = c.e == 2 ? 1 : 3;
-  XentPrep a{c.a.x, c.a.ldx, f.t, f.k, f.tp, nullptr, 0, 0, nullptr, 0};
+  XentPrep a{c.a.x, c.a.ldx, f.t, f.k, f.tp, nullptr, 0, 0, nullptr, 0, 0};
   f.x = c.a.x;
   f.ldx = c.a.ldx;
   f.kx = f.k;
@@ -134,12 +136,12 @@ hipError_t few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed,
     f.xt = a.xt;
     f.xtplane = a.xtplane;
   }
-  return r.go && (a.xp || a.xt) ? launch_few_prep(a, c.e == 4, r.st) : hipSuccess;
+  return a;
 }
 
 // Workgroups of z's kernel: up to four per CU, which then take several blocks
-// of 16 rows in turn.
-int64_t few_groups(int64_t n) { return std::min<int64_t>(lin_cdiv(n, kXentGroup), 1024); }
+// of rows in turn.
+int64_t few_groups(int64_t n, int rt) { return std::min<int64_t>(lin_cdiv(n, 16 * rt), 1024); }
 
 hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const dion_cross_entropy& a = c.a;
@@ -150,7 +152,8 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const bool copy = !few && !lin_direct(c.w);
   const int64_t piece = copy ? xent_piece(a.n, 2 * planes * lin_cdiv(a.k, 64) * 64) : a.n;
   // one partial column per 64 columns at least
-  const int64_t most = few ? few_groups(a.n) : lin_cdiv(a.n, 64) + 2 * lin_cdiv(a.n, piece);
+  const int rt = few_rows(static_cast<int>(a.t), c.e == 4, a.n);
+  const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 2 * lin_cdiv(a.n, piece);
   XentEpi e{};
   e.target = a.target;
   e.ignore = a.ignore_index;
@@ -164,8 +167,9 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
     cols = most;
     XentFew f = few_args(c, c.w);
     const bool raw = a.t <= 16 && !lin_direct(c.x);
-    LIN_TRY(few_prep(r, c, !raw, false, f));
-    if (r.go) LIN_TRY(launch_few_z(f, e, c.e == 4, false, raw, static_cast<int>(cols), r.st));
+    const XentPrep prep = few_prep(r, c, !raw, false, f);
+    if (r.go && prep.xp) LIN_TRY(launch_few_prep(prep, c.e == 4, r.st));
+    if (r.go) LIN_TRY(launch_few_z(f, e, prep, c.e == 4, false, raw, rt, static_cast<int>(cols), r.st));
   } else {
     Operand x;
     lin_operand(r, c.x, x);
@@ -216,7 +220,7 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
   XentFew f = few_args(c, c.w);
   const int64_t piece = xent_piece(a.n, 2 * planes * (a.t + f.tp));
   XentEpi e = xent_grad(c, planes, a.t, piece);
-  LIN_TRY(few_prep(r, c, true, a.dw != nullptr, f));
+  XentPrep prep = few_prep(r, c, true, a.dw != nullptr, f);
   e.dz = r.ws.take<uint16_t>(planes * e.plane);
   f.dztplane = e.pitch * f.tp;
   f.dzt = r.ws.take<uint16_t>(planes * f.dztplane);
@@ -225,24 +229,35 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
   const int64_t parts = std::max<int64_t>(1, std::min(lin_cdiv(1024, across), lin_cdiv(piece, 128)));
   float* part = a.dx ? r.ws.take<float>(pieces * parts * a.t * a.k) : nullptr;
   if (!r.go) return hipSuccess;
+  if (prep.xp) {   // both forms of x before z; else the transpose beside it
+    LIN_TRY(launch_few_prep(prep, f32, r.st));
+    prep.xt = nullptr;
+  }
+  XentDxSum sum{part, static_cast<int32_t>(pieces * parts), f.t, f.k, a.dx, a.lddx, !f32};
   for (int64_t p = 0; p < pieces; ++p) {
     const int64_t j0 = p * piece;
     const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
     f.w = wj.p;
     f.n = static_cast<int32_t>(wj.rows);
     e.j0 = static_cast<int32_t>(j0);
-    LIN_TRY(launch_few_z(f, e, f32, true, false, static_cast<int>(few_groups(e.pitch)), r.st));
+    const int rt = few_rows(f.t, f32, e.pitch);
+    prep.first = static_cast<int32_t>(few_groups(e.pitch, rt));
+    LIN_TRY(launch_few_z(f, e, prep, f32, true, false, rt, 0, r.st));
+    prep.xt = nullptr;
     if (a.dx) LIN_TRY(launch_few_dx(f, e, f32, static_cast<int>(parts), part + p * parts * a.t * a.k, r.st));
+    const bool last = p + 1 == pieces;
     if (a.dw) {
       const Span dj = xent_rows(c.dw, j0, wj.rows);
       // about four workgroups per CU again, in whole steps of 64 columns
       const int64_t down = lin_cdiv(wj.rows, 4 * kFewDwRows);
       const int64_t split = std::min(lin_cdiv(a.k, 64), lin_cdiv(1024, down));
-      const XentDw d{const_cast<void*>(dj.p), a.lddw, static_cast<int32_t>(lin_cdiv(lin_cdiv(a.k, split), 64) * 64), a.accumulate};
-      LIN_TRY(launch_few_dw(f, d, f32, r.st));
+      const XentDw d{const_cast<void*>(dj.p), a.lddw, static_cast<int32_t>(lin_cdiv(lin_cdiv(a.k, split), 64) * 64), a.accumulate, 0, 0};
+      LIN_TRY(launch_few_dw(f, d, last ? sum : XentDxSum{}, f32, r.st));
+    } else if (last) {
+      LIN_TRY(launch_few_dxsum(sum, r.st));
     }
   }
-  return a.dx ? launch_few_dxsum(f, part, static_cast<int>(pieces * parts), a.dx, a.lddx, !f32, r.st) : hipSuccess;
+  return hipSuccess;
 }
 
 hipError_t xent_backward(XentRun& r, const XentCall& c) {

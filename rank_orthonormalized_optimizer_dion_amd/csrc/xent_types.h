@@ -49,9 +49,11 @@ struct XentJoin {
 inline int64_t xent_tile_cols(int64_t ty) { return 2 * ty; }   // two wavefronts across a tile
 
 // Few tokens (k_xent_few.hip).
-constexpr int kXentFewBf16 = 64, kXentFewF32 = 128;   // tokens
-constexpr int kXentGroup = 16;     // rows of W that a workgroup turns into z at a time
-constexpr int kFewDwRows = 64;     // rows of dW of a wavefront (half of it beyond 64 tokens)
+// tokens; with a bfloat16 x and W of whole 16-byte pieces, which the tiles read
+// in place, half as many (2048 -> 32000, gradients: 32 tokens 114 us, 64 tokens
+// 163 and as tiles 151; 768 -> 50257: 64 tokens 148, as tiles 113)
+constexpr int kXentFew = 64, kXentFewDirect = 32;
+constexpr int kFewDwRows = 64;     // rows of dW of a wavefront
 struct XentFew {
   const void* w;           // n rows of k
   int64_t ldw;
@@ -59,7 +61,7 @@ struct XentFew {
   const void* x;           // t rows: planes in bfloat16, 16-byte aligned, or x itself
   int64_t ldx, xplane;
   int32_t kx;              // columns that are there (and zero from k on)
-  int32_t tp;              // tokens of the transposed operands: t up to 32, 64 or 128
+  int32_t tp;              // tokens of the transposed operands: 32 or 64
   const uint16_t* xt;      // planes of k x tp
   int64_t xtplane;
   uint16_t* dzt;           // planes of pitch x tp
@@ -73,21 +75,32 @@ struct XentPrep {
   int64_t ldp, xplane;
   uint16_t* xt;            // or null
   int64_t xtplane;
+  int32_t first;           // workgroups of dz's launch before those that make xt
 };
 struct XentDw {
   void* dw;
   int64_t ld;
   int32_t cols;            // of a workgroup
   int32_t accumulate;
+  int32_t down, tiles;     // workgroups down the rows, and in all (set at the launch)
 };
-// raw: x as it is (at most 16 tokens, no grad); groups: workgroups, each of
-// which leaves one partial column
-hipError_t launch_few_z(const XentFew& f, const XentEpi& e, bool f32, bool grad, bool raw, int groups, hipStream_t st);
+struct XentDxSum {
+  const float* part;       // `parts` times t x k
+  int32_t parts, t, k;
+  void* dx;                // or null: nothing to do
+  int64_t ld;
+  int32_t dtype;
+};
+// Blocks of 16 rows of W that a workgroup turns into z at a time.
+int few_rows(int t, bool f32, int64_t n);
+// raw: x as it is (at most 16 tokens, no grad); groups: forward's workgroups,
+// each of which leaves one partial column; prep (grad): first, and xt or null
+hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool f32, bool grad, bool raw, int rt,
+                        int groups, hipStream_t st);
 hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st);
 hipError_t launch_few_dx(const XentFew& f, const XentEpi& e, bool f32, int parts, float* part, hipStream_t st);
-hipError_t launch_few_dxsum(const XentFew& f, const float* part, int parts, void* dx, int64_t lddx, int dtype,
-                            hipStream_t st);
-hipError_t launch_few_dw(const XentFew& f, const XentDw& d, bool f32, hipStream_t st);
+hipError_t launch_few_dxsum(const XentDxSum& s, hipStream_t st);
+hipError_t launch_few_dw(const XentFew& f, const XentDw& d, const XentDxSum& sum, bool f32, hipStream_t st);
 
 // z by tiles; grad: backward.
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st);

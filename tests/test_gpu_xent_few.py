@@ -1,7 +1,7 @@
-"""The cross entropy of few tokens (GPU): its own kernels up to 64 tokens in
-bfloat16 and 128 in float32, on both sides of each of their block sizes, at
-every alignment, with short and long vocabularies and reductions.  Same checks
-and tolerances as the other sizes."""
+"""The cross entropy of few tokens (GPU): its own kernels up to 64 tokens (32
+where the tiles can read x and W in place), on both sides of each of their block
+sizes, at every alignment, with short and long vocabularies and reductions.
+Same checks and tolerances as the other sizes."""
 import pytest
 
 from .gpuhelp import say
