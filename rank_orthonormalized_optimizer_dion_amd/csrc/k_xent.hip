@@ -12,134 +12,14 @@
 // of the vocabulary together.  Backward: z once more, turned into dz in the
 // accumulators and written in bfloat16, a piece of the vocabulary at a time,
 // for the two products that follow (k_lin_mm).
-#include <utility>
-
 #include "dion.h"
 #include "lin_device.h"
 #include "work16.h"
-#include "xent_device.h"
+#include "xent_tile.h"
 
 namespace dion {
 
 namespace {
-
-// f(integral_constant 0), f(1), ...: DPP controls have to be constants.
-template <class F, int... I>
-__device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void each(F f) {
-  each(f, std::make_integer_sequence<int, N>{});
-}
-
-// Eight values of dz as bfloat16 planes.
-__device__ __forceinline__ void store_dz(const XentEpi& e, int64_t row, int col, const float (&v)[8]) {
-  uint16_t* at = e.dz + row * e.pitch + col;
-  float rest[8];
-  uint16_t h[8];
-  for (int pl = 0; pl < e.planes; ++pl) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = pinned(pl == 0 ? v[k] : rest[k]);
-      h[k] = pl == 0 && e.planes > 1 ? first_plane(x) : to_bf16(x);
-      rest[k] = x - bf16_to_f32(h[k]);
-    }
-    *reinterpret_cast<u32x4*>(at + pl * e.plane) = pack8(h);
-  }
-}
-
-// The accumulators of a wavefront hold 64 rows; lane l keeps the data of row
-// 16 (l % 16 / 4) + 4 (l / 16) + l % 4, which accumulator row (m, v) of its 16
-// lanes asks lane 4 m + v of them for (row_newbcast).
-__device__ __forceinline__ int own_row(int lane) { return 16 * ((lane & 15) >> 2) + 4 * (lane >> 4) + (lane & 3); }
-constexpr int kBcast = 0x150;   // DPP row_newbcast: of lane 0
-
-template <class S>
-__device__ __forceinline__ void stats_tile(typename S::Acc (&acc)[S::FM][S::FN], const XentEpi& e, int t, int n,
-                                           int row0, int col0, int part) {
-  const int lane = threadIdx.x & 63, l15 = lane & 15;
-  const int own = row0 + own_row(lane);
-  // the target's column, counted from this wavefront's first
-  int local = -1;
-  if (own < t) {
-    const int64_t y = e.target[own] - e.j0 - col0;
-    if (y >= 0 && y < S::TN && col0 + y < n) local = static_cast<int>(y);
-  }
-  const bool any = __ballot(local >= 0) != 0;
-  if (any)
-    each<4 * S::FM>([&](auto i) {
-      constexpr int m = i / 4, v = i % 4;
-      const int want = dpp<kBcast + i>(local);
-#pragma unroll
-      for (int q = 0; q < S::FN; ++q)
-        if (want == S::F * q + l15) e.hit[row0 + S::F * m + 4 * (lane >> 4) + v] = acc[m][q][v];
-    });
-  const bool edge = col0 + S::TN > n;
-  float top = 0.0f, sum = 0.0f, total = 0.0f;
-  each<4 * S::FM>([&](auto i) {
-    constexpr int m = i / 4, v = i % 4;
-    float z[S::FN];
-#pragma unroll
-    for (int q = 0; q < S::FN; ++q) z[q] = acc[m][q][v];
-    if (e.total) {
-      float s = 0.0f;
-#pragma unroll
-      for (int q = 0; q < S::FN; ++q) s += !edge || col0 + S::F * q + l15 < n ? z[q] : 0.0f;
-      s = row_sum(s);
-      total = l15 == i ? s : total;
-    }
-    if (edge) {
-#pragma unroll
-      for (int q = 0; q < S::FN; ++q) z[q] = col0 + S::F * q + l15 < n ? z[q] : -INFINITY;
-    }
-    float hi = z[0];
-#pragma unroll
-    for (int q = 1; q < S::FN; ++q) hi = fmaxf(hi, z[q]);
-    hi = row_max(hi);
-    const float b = base_of(hi);
-    float s = 0.0f;
-#pragma unroll
-    for (int q = 0; q < S::FN; ++q) s += exp_fast(z[q] - b);
-    s = row_sum(s);
-    top = l15 == i ? hi : top;
-    sum = l15 == i ? s : sum;
-  });
-  if (own < t) {
-    const int64_t at = static_cast<int64_t>(part) * t + own;
-    e.top[at] = top;
-    e.sum[at] = sum;
-    if (e.total) e.total[at] = total;
-  }
-}
-
-template <class S>
-__device__ __forceinline__ void dz_tile(typename S::Acc (&acc)[S::FM][S::FN], const XentEpi& e, int t, int n,
-                                        int row0, int col0) {
-  const int lane = threadIdx.x & 63, l15 = lane & 15;
-  int64_t y;
-  const XentRow r = xent_row(e, row0 + own_row(lane), t, y);
-  y -= e.j0 + col0;
-  const int local = y >= 0 && y < S::TN ? static_cast<int>(y) : -1;
-  const bool any = __ballot(local >= 0) != 0, edge = col0 + S::TN > n;
-  each<4 * S::FM>([&](auto i) {
-    constexpr int m = i / 4, v = i % 4;
-    const float lse = dpp<kBcast + i>(r.lse), a = dpp<kBcast + i>(r.a), b = dpp<kBcast + i>(r.b);
-    const int mask = dpp<kBcast + i>(r.mask);
-#pragma unroll
-    for (int q = 0; q < S::FN; ++q) acc[m][q][v] = dz_of(acc[m][q][v], lse, a, b, mask);
-    if (any) {
-      const int want = dpp<kBcast + i>(local);
-      const float c = dpp<kBcast + i>(r.c);
-#pragma unroll
-      for (int q = 0; q < S::FN; ++q) acc[m][q][v] -= want == S::F * q + l15 ? c : 0.0f;
-    }
-    if (edge) {
-#pragma unroll
-      for (int q = 0; q < S::FN; ++q) acc[m][q][v] = col0 + S::F * q + l15 < n ? acc[m][q][v] : 0.0f;
-    }
-  });
-}
 
 template <int TILE, bool GRAD>
 __global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e) {
@@ -168,7 +48,12 @@ __global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e
         acc, smem, [](int, int) { return NoPre{}; },
         [&](int r, int q, const float (&v)[8], const NoPre&) {
           const int row = r0 + r, col = c0 + q;
-          if (row < e.prows && col < e.pitch) store_dz(e, row, col, v);
+          if (row < e.prows && col < e.pitch) {   // zero past the piece's columns and rows
+            uint16_t h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = to_bf16(v[k]);
+            *reinterpret_cast<u32x4*>(e.dz + row * e.pitch + col) = pack8(h);
+          }
         });
   } else {
     stats_tile<S>(acc, e, p.M, p.N, row0, col0, e.col0 + 2 * tj + wave % S::WN);

@@ -1,0 +1,110 @@
+// The cross entropy's products in float32 (mm32.h): z with the epilogues of
+// k_xent.hip, dz kept in float32, dx = dz W and dW = dz^T x.
+#include "dion.h"
+#include "mm32.h"
+#include "work16.h"
+#include "xent_tile.h"
+
+namespace dion {
+
+namespace {
+
+enum Kind32 { kZ = 0, kDx, kDw };   // K-major both; K-major, x-major; x-major both
+
+template <Kind32 KIND, bool GRAD>
+__global__ __launch_bounds__(512, 2) void k_f32_mm(XentProduct32 p, XentEpi e) {
+  using S = Shape32<KIND == kDw, KIND != kZ>;
+  static_assert(S::TM == 64 && S::F == 16, "rows of a wavefront");
+  __shared__ u32x4 smem[S::LDS_CELLS];
+  const Work16 work{p.full, p.tx * p.ty - p.full, p.slices, p.part, p.count};
+  const Item16 it = item16(work, xcd_item(blockIdx.x, gridDim.x));
+  int ti, tj;
+  tile_order(it.tile, p.tx, p.ty, ti, tj);
+  const int r0 = ti * S::BM, c0 = tj * S::BN;
+  int kbeg, kend;
+  slice16<S>(it, p.K, kbeg, kend);
+  typename S::Acc acc[S::FM][S::FN];
+  typename S::TA ta;
+  typename S::TB tb;
+  ta.init(p.a, p.lda, r0, p.M);
+  tb.init(p.b, p.ldb, c0, p.N);
+  tile_product32<S>(ta, tb, S::TA::whole(r0, p.M) && S::TB::whole(c0, p.N), kbeg, kend, smem, acc);
+  if (!join16<S>(work, it, smem, acc)) return;
+  if constexpr (KIND == kZ) {
+    const int wave = wave16();
+    const int row0 = r0 + (wave / S::WN) * S::TM, col0 = c0 + (wave % S::WN) * S::TN;
+    if constexpr (GRAD) {
+      dz_tile<S>(acc, e, p.M, p.N, row0, col0);
+      tile_runs<S, false>(
+          acc, smem, [](int, int) { return NoPre{}; },
+          [&](int r, int q, const float (&v)[8], const NoPre&) {
+            const int row = r0 + r, col = c0 + q;
+            if (row < p.M && col < e.pitch) {   // zero past the piece's columns
+              float* at = e.dz32 + row * e.pitch + col;
+              *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+              *reinterpret_cast<f32x4*>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            }
+          });
+    } else {
+      stats_tile<S>(acc, e, p.M, p.N, row0, col0, e.col0 + S::WN * tj + wave % S::WN);
+    }
+  } else {
+    struct Pre {
+      float v[8];
+    };
+    tile_runs<S, false>(
+        acc, smem,
+        [&](int r, int q) {
+          Pre o{};
+          const int row = r0 + r, col = c0 + q;
+          if (p.accumulate && row < p.M && col < p.N) {
+            const float* at = p.out + row * p.ldo + col;
+            if (col + 8 <= p.N) {
+              __builtin_memcpy(o.v, at, 32);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o.v[i] = col + i < p.N ? at[i] : 0.0f;
+            }
+          }
+          return o;
+        },
+        [&](int r, int q, const float (&v)[8], const Pre& old) {
+          const int row = r0 + r, col = c0 + q;
+          if (row >= p.M || col >= p.N) return;
+          float* at = p.out + row * p.ldo + col;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = v[i] + old.v[i];
+          if (col + 8 <= p.N) {
+            __builtin_memcpy(at, o, 32);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (col + i < p.N) at[i] = o[i];
+          }
+        });
+  }
+}
+
+__global__ __launch_bounds__(512) void k_f32_counts(uint32_t* count) { count[threadIdx.x] = 0; }
+
+}  // namespace
+
+hipError_t launch_xent_counts(uint32_t* count, hipStream_t st) {
+  static_assert(kTileSlots256 <= 512, "one counter per thread");
+  k_f32_counts<<<dim3(1), dim3(512), 0, st>>>(count);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 kind, hipStream_t st) {
+  const dim3 grid(p.items), block(512);
+  switch (kind) {
+    case kXentStats32: k_f32_mm<kZ, false><<<grid, block, 0, st>>>(p, e); break;
+    case kXentDz32: k_f32_mm<kZ, true><<<grid, block, 0, st>>>(p, e); break;
+    case kXentDx32: k_f32_mm<kDx, false><<<grid, block, 0, st>>>(p, e); break;
+    default: k_f32_mm<kDw, false><<<grid, block, 0, st>>>(p, e); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace dion

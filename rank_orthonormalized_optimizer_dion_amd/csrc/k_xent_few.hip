@@ -20,6 +20,7 @@
 // with float32.
 #include "dion.h"
 #include "lin_device.h"
+#include "mm32.h"
 #include "xent_device.h"
 #include "xent_types.h"
 
@@ -42,20 +43,8 @@ struct Planes8 {
   u32x4 p[PL];
 };
 __device__ __forceinline__ Planes8<3> split8(const float (&v)[8]) {
-  Planes8<3> o;
-  float rest[8];
-  uint16_t h[8];
-#pragma unroll
-  for (int pl = 0; pl < 3; ++pl) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = pinned(pl == 0 ? v[k] : rest[k]);
-      h[k] = pl == 0 ? first_plane(x) : to_bf16(x);
-      rest[k] = x - bf16_to_f32(h[k]);
-    }
-    o.p[pl] = pack8(h);
-  }
-  return o;
+  const Split8 s = split_planes(v);
+  return {{s.p[0], s.p[1], s.p[2]}};
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {

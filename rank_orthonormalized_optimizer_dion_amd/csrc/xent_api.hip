@@ -95,6 +95,10 @@ struct XentRun : Run {
     if (!this->go || (this->Run::packs.n == 0 && this->Run::packs.counts == 0)) return hipSuccess;
     return launch_lin_packs(this->Run::packs, st);
   }
+  hipError_t counts32() {   // the counters of a call's cut tiles, once
+    if (!this->go || this->Run::packs.counts == 0) return hipSuccess;
+    return launch_xent_counts(this->Run::packs.count, st);
+  }
   void done() {
     peak = std::max(peak, ws.used);
     Run::packs.n = 0;
@@ -143,17 +147,43 @@ XentPrep few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed, X
 // of rows in turn.
 int64_t few_groups(int64_t n, int rt) { return std::min<int64_t>(lin_cdiv(n, 16 * rt), 1024); }
 
+// One float32 product, cut along long reductions as the other tiles are: a
+// stage is six products of half a 256 x 256 tile.
+XentProduct32 xent_product32(XentRun& r, const float* A, int64_t lda, const float* B, int64_t ldb, int64_t M, int64_t N,
+                             int64_t K) {
+  XentProduct32 p{};
+  p.a = A;
+  p.b = B;
+  p.lda = lda;
+  p.ldb = ldb;
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(N);
+  p.K = static_cast<int32_t>(K);
+  p.tx = static_cast<int32_t>(lin_cdiv(M, kXentM32));
+  p.ty = static_cast<int32_t>(lin_cdiv(N, kXentN32));
+  const Cut16 c = cut_tiles(static_cast<int64_t>(p.tx) * p.ty, 256, lin_cdiv(K, kLinStage) * 3);
+  p.items = static_cast<int32_t>(c.items());
+  p.full = static_cast<int32_t>(c.full);
+  p.slices = static_cast<int32_t>(c.slices);
+  if (c.cut) {
+    p.part = r.ws.take<float>(c.cut * c.slices * kXentM32 * kXentN32);
+    p.count = r.Run::packs.count;
+    r.Run::packs.counts = 1;
+  }
+  return p;
+}
+
 hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const dion_cross_entropy& a = c.a;
   if (a.t == 0) return hipSuccess;
   const bool few = xent_few(c);
-  const int planes = c.e == 2 ? 1 : 3;
+  const bool f32 = !few && c.e == 4;
   // a piece at a time only where W has to be copied
-  const bool copy = !few && !lin_direct(c.w);
-  const int64_t piece = copy ? xent_piece(a.n, 2 * planes * lin_cdiv(a.k, 64) * 64) : a.n;
+  const bool copy = !few && !f32 && !lin_direct(c.w);
+  const int64_t piece = copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n;
   // one partial column per 64 columns at least
   const int rt = few_rows(static_cast<int>(a.t), c.e == 4, a.n);
-  const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 2 * lin_cdiv(a.n, piece);
+  const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4 * lin_cdiv(a.n, piece);
   XentEpi e{};
   e.target = a.target;
   e.ignore = a.ignore_index;
@@ -170,6 +200,12 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
     const XentPrep prep = few_prep(r, c, !raw, false, f);
     if (r.go && prep.xp) LIN_TRY(launch_few_prep(prep, c.e == 4, r.st));
     if (r.go) LIN_TRY(launch_few_z(f, e, prep, c.e == 4, false, raw, rt, static_cast<int>(cols), r.st));
+  } else if (f32) {
+    const XentProduct32 z = xent_product32(r, static_cast<const float*>(a.x), a.ldx, static_cast<const float*>(a.w), a.ldw,
+                                           a.t, a.n, a.k);
+    cols = xent_tile_cols32(z.ty);
+    LIN_TRY(r.counts32());
+    if (r.go) LIN_TRY(launch_xent_f32(z, e, kXentStats32, r.st));
   } else {
     Operand x;
     lin_operand(r, c.x, x);
@@ -179,8 +215,8 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
       const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
       Operand w;
       lin_operand(r, wj, w);
-      const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, !lin_direct(c.x) && !lin_direct(c.w), planes == 3 ? 6 : 1,
-                                    kLinForward, LinOut{});
+      const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, !lin_direct(c.x) && !lin_direct(c.w), 1, kLinForward,
+                                    LinOut{});
       e.j0 = static_cast<int32_t>(j0);
       e.col0 = static_cast<int32_t>(cols);
       cols += xent_tile_cols(z.p.ty);
@@ -260,30 +296,55 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
   return hipSuccess;
 }
 
-hipError_t xent_backward(XentRun& r, const XentCall& c) {
+hipError_t xent_backward_f32(XentRun& r, const XentCall& c) {
   const dion_cross_entropy& a = c.a;
-  if (!a.dx && !a.dw) return hipSuccess;
-  const bool f32 = c.e == 4;
-  LinOut out{};
-  out.dtype = !f32;
-  if (a.t == 0) {   // no tokens: dW is zero
-    if (!a.dw || a.accumulate) return hipSuccess;
-    out.y = a.dw;
-    out.ldy = a.lddw;
-    const Product dw = lin_product(r, Operand{}, Operand{}, a.n, a.k, 0, false, 1, kLinDw, out);
-    LIN_TRY(r.packs());
-    return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
+  const int64_t piece = xent_piece(a.n, 4 * a.t);
+  XentEpi e = xent_grad(c, 1, a.t, piece);
+  e.dz32 = r.ws.take<float>(a.t * e.pitch);
+  const float* x = static_cast<const float*>(a.x);
+  const size_t mark = r.ws.used;
+  for (int64_t j0 = 0; j0 < a.n; j0 += piece) {
+    r.ws.used = mark;
+    const int64_t n = std::min(piece, a.n - j0);
+    const float* w = static_cast<const float*>(xent_rows(c.w, j0, n).p);
+    const XentProduct32 z = xent_product32(r, x, a.ldx, w, a.ldw, a.t, n, a.k);
+    XentProduct32 dx{}, dw{};
+    if (a.dx) {
+      dx = xent_product32(r, e.dz32, e.pitch, w, a.ldw, a.t, a.k, n);
+      dx.out = static_cast<float*>(a.dx);
+      dx.ldo = a.lddx;
+      dx.accumulate = j0 > 0;
+    }
+    if (a.dw) {
+      dw = xent_product32(r, e.dz32, e.pitch, x, a.ldx, n, a.k, a.t);
+      dw.out = static_cast<float*>(const_cast<void*>(xent_rows(c.dw, j0, n).p));
+      dw.ldo = a.lddw;
+      dw.accumulate = a.accumulate != 0;
+    }
+    e.j0 = static_cast<int32_t>(j0);
+    if (j0 == 0) LIN_TRY(r.counts32());   // every launch leaves them cleared
+    if (r.go) {
+      LIN_TRY(launch_xent_f32(z, e, kXentDz32, r.st));
+      if (a.dx) LIN_TRY(launch_xent_f32(dx, e, kXentDx32, r.st));
+      if (a.dw) LIN_TRY(launch_xent_f32(dw, e, kXentDw32, r.st));
+    }
+    r.peak = std::max(r.peak, r.ws.used);
   }
-  if (xent_few(c)) return xent_backward_few(r, c);
-  const int planes = f32 ? 3 : 1, nseg = f32 ? 6 : 1;
+  return hipSuccess;
+}
+
+hipError_t xent_backward_bf16(XentRun& r, const XentCall& c) {
+  const dion_cross_entropy& a = c.a;
+  LinOut out{};
+  out.dtype = 1;
   const int64_t prows = lin_cdiv(a.t, kLinStage) * kLinStage;
-  const int64_t wcopy = lin_direct(c.w) ? 0 : 2 * planes * lin_cdiv(a.k, 64) * 64;
-  const int64_t piece = xent_piece(a.n, std::max(2 * planes * prows, wcopy));
-  XentEpi e = xent_grad(c, planes, prows, piece);
-  e.dz = r.ws.take<uint16_t>(planes * e.plane);
-  const Operand dz{e.dz, e.pitch, e.plane};
+  const int64_t wcopy = lin_direct(c.w) ? 0 : 2 * lin_cdiv(a.k, 64) * 64;
+  const int64_t piece = xent_piece(a.n, std::max(2 * prows, wcopy));
+  XentEpi e = xent_grad(c, 1, prows, piece);
+  e.dz = r.ws.take<uint16_t>(e.plane);
+  const Operand dz{e.dz, e.pitch, 0};
   // dx over several pieces is summed in float32
-  const bool sum = a.dx && piece < a.n && !f32;
+  const bool sum = a.dx && piece < a.n;
   float* dxsum = sum ? r.ws.take<float>(a.t * a.k) : nullptr;
   Operand x{};
   lin_operand(r, c.x, x);
@@ -296,7 +357,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
     Operand w{};
     lin_operand(r, wj, w);
     Product dx{}, dw{};
-    const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, padded && xpadded, nseg, kLinForward, LinOut{});
+    const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, padded && xpadded, 1, kLinForward, LinOut{});
     if (a.dx) {
       LinOut o = out;
       o.y = a.dx;
@@ -312,7 +373,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
         o.ldr = a.k;
         o.wide = 1;
       }
-      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, padded, nseg, kLinDx, o);
+      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, padded, 1, kLinDx, o);
     }
     if (a.dw) {
       LinOut o = out;
@@ -320,7 +381,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
       o.y = const_cast<void*>(dj.p);
       o.ldy = a.lddw;
       o.accumulate = a.accumulate != 0;
-      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, xpadded, nseg, kLinDw, o);
+      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, xpadded, 1, kLinDw, o);
     }
     e.j0 = static_cast<int32_t>(j0);
     LIN_TRY(r.packs());
@@ -332,6 +393,24 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
     r.done();
   }
   return hipSuccess;
+}
+
+hipError_t xent_backward(XentRun& r, const XentCall& c) {
+  const dion_cross_entropy& a = c.a;
+  if (!a.dx && !a.dw) return hipSuccess;
+  const bool f32 = c.e == 4;
+  LinOut out{};
+  out.dtype = !f32;
+  if (a.t == 0) {   // no tokens: dW is zero
+    if (!a.dw || a.accumulate) return hipSuccess;
+    out.y = a.dw;
+    out.ldy = a.lddw;
+    const Product dw = lin_product(r, Operand{}, Operand{}, a.n, a.k, 0, false, 1, kLinDw, out);
+    LIN_TRY(r.packs());
+    return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
+  }
+  if (xent_few(c)) return xent_backward_few(r, c);
+  return f32 ? xent_backward_f32(r, c) : xent_backward_bf16(r, c);
 }
 
 template <class Go>

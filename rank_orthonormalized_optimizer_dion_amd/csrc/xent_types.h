@@ -28,6 +28,7 @@ struct XentEpi {
   float keep, share;       // 1 - smoothing, smoothing / vocab
   float slope;             // 2 z-loss
   uint16_t* dz;
+  float* dz32;             // float32 tiles: dz as it is
   int64_t pitch, plane;    // elements from row to row, from plane to plane
   int32_t prows, planes;
 };
@@ -45,8 +46,28 @@ struct XentJoin {
   float keep, smoothing, z_loss;
 };
 
-// Partial columns of a launch of tiles.
-inline int64_t xent_tile_cols(int64_t ty) { return 2 * ty; }   // two wavefronts across a tile
+// Partial columns of a launch of tiles: one per wavefront across a tile.
+inline int64_t xent_tile_cols(int64_t ty) { return 2 * ty; }
+inline int64_t xent_tile_cols32(int64_t ty) { return 4 * ty; }
+
+// float32 tiles (mm32.h): C (M x N) = sum of A B^T over K.
+constexpr int kXentM32 = 128, kXentN32 = 256;
+struct XentProduct32 {
+  const float* a;
+  const float* b;
+  int64_t lda, ldb;
+  int32_t M, N, K;
+  int32_t tx, ty, items;   // workgroups
+  int32_t full, slices;    // mm16.h, Work16
+  float* part;
+  uint32_t* count;
+  float* out;              // dx, dW
+  int64_t ldo;
+  int32_t accumulate;
+};
+enum XentKind32 { kXentStats32 = 0, kXentDz32, kXentDx32, kXentDw32 };
+hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 kind, hipStream_t st);
+hipError_t launch_xent_counts(uint32_t* count, hipStream_t st);   // clears kTileSlots256
 
 // Few tokens (k_xent_few.hip).
 // tokens; with a bfloat16 x and W of whole 16-byte pieces, which the tiles read
