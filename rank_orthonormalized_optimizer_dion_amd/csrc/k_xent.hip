@@ -12,6 +12,8 @@
 // of the vocabulary together.  Backward: z once more, turned into dz in the
 // accumulators and written in bfloat16, a piece of the vocabulary at a time,
 // for the two products that follow (k_lin_mm).
+#include <algorithm>
+
 #include "dion.h"
 #include "lin_device.h"
 #include "work16.h"
@@ -110,6 +112,37 @@ __global__ __launch_bounds__(256) void k_xent_join(XentJoin j) {
   j.loss[row] = loss;
 }
 
+// Copies of bfloat16 operands whose rows the tiles cannot read in place: 16
+// bytes per thread and step, zero past the columns and (to the last whole
+// stage) past the rows.  32000 x 1999: @@.
+__global__ __launch_bounds__(256) void k_xent_copy(XentCopies a) {
+  const int which = static_cast<int>(blockIdx.x) >= a.c[0].blocks;
+  const XentCopy c = a.c[which];
+  if (blockIdx.x == 0 && a.count)
+    for (int i = threadIdx.x; i < kTileSlots128; i += 256) a.count[i] = 0;
+  const int64_t cells = c.pitch / 8, total = c.prows * cells, step = static_cast<int64_t>(c.blocks) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - (which ? a.c[0].blocks : 0)) * 256 + threadIdx.x; i < total; i += 4 * step) {
+    u32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t at = i + u * step, row = at / cells;
+      const int col = static_cast<int>(at - row * cells) * 8, left = at < total && row < c.rows ? c.cols - col : 0;
+      const uint16_t* p = c.src + row * c.ld + col;
+      if (left >= 8) {
+        __builtin_memcpy(&v[u], p, 16);
+      } else {
+        uint16_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = k < left ? p[k] : 0;
+        v[u] = pack8(h);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * step < total) *reinterpret_cast<u32x4*>(c.dst + (i + u * step) * 8) = v[u];
+  }
+}
+
 template <int TILE>
 hipError_t product(const LinProduct& p, const XentEpi& e, bool grad, hipStream_t st) {
   if (grad) k_xent_mm<TILE, true><<<dim3(p.items), dim3(2 * TILE), 0, st>>>(p, e);
@@ -122,6 +155,16 @@ hipError_t product(const LinProduct& p, const XentEpi& e, bool grad, hipStream_t
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st) {
   if (tile == 256) return product<256>(p, e, grad, st);
   return product<128>(p, e, grad, st);
+}
+
+hipError_t launch_xent_copies(XentCopies a, hipStream_t st) {
+  int blocks = 0;
+  for (XentCopy& c : a.c) {
+    c.blocks = static_cast<int32_t>(std::min<int64_t>((c.prows * (c.pitch / 8) + 1023) / 1024, 4096));
+    blocks += c.blocks;
+  }
+  k_xent_copy<<<dim3(blocks > 0 ? blocks : 1), dim3(256), 0, st>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_xent_join(const XentJoin& j, hipStream_t st) {

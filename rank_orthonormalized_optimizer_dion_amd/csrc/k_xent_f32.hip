@@ -29,6 +29,16 @@ __global__ __launch_bounds__(512, 2) void k_f32_mm(XentProduct32 p, XentEpi e) {
   ta.init(p.a, p.lda, r0, p.M);
   tb.init(p.b, p.ldb, c0, p.N);
   tile_product32<S>(ta, tb, S::TA::whole(r0, p.M) && S::TB::whole(c0, p.N), kbeg, kend, smem, acc);
+  if constexpr (KIND != kZ) {
+    if (p.apart && it.slices > 1) {   // k_f32_join's
+      f32x4* at = reinterpret_cast<f32x4*>(p.part) + (static_cast<int64_t>(it.cut) * it.slices + it.slice) * (S::BM * S::BN / 4) + threadIdx.x;
+#pragma unroll
+      for (int m = 0; m < S::FM; ++m)
+#pragma unroll
+        for (int n = 0; n < S::FN; ++n) at[(m * S::FN + n) * S::NT] = acc[m][n];
+      return;
+    }
+  }
   if (!join16<S>(work, it, smem, acc)) return;
   if constexpr (KIND == kZ) {
     const int wave = wave16();
@@ -86,15 +96,36 @@ __global__ __launch_bounds__(512, 2) void k_f32_mm(XentProduct32 p, XentEpi e) {
   }
 }
 
-__global__ __launch_bounds__(512) void k_f32_counts(uint32_t* count) { count[threadIdx.x] = 0; }
+// The slices of cut tiles, in order: a workgroup per 1/8 of a tile (two pieces
+// of each thread's accumulators).  dx of 515 tokens, 10007 -> 517, 17 slices: @@.
+__global__ __launch_bounds__(512) void k_f32_join(XentProduct32 p) {
+  using S = Shape32<false, true>;   // the accumulators' layout is the same in both kinds
+  constexpr int PARTS = S::FM * S::FN / 2;
+  const int cut = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
+  const f32x4* at = reinterpret_cast<const f32x4*>(p.part) + static_cast<int64_t>(cut) * p.slices * (S::BM * S::BN / 4) + threadIdx.x;
+  f32x4 sum[2] = {};
+#pragma unroll 4
+  for (int s = 0; s < p.slices; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] += at[s * (S::BM * S::BN / 4) + (2 * part + i) * S::NT];
+  int ti, tj;
+  tile_order(p.full + cut, p.tx, p.ty, ti, tj);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = (2 * part + i) / S::FN, n = (2 * part + i) % S::FN;
+    const int row = ti * S::BM + (wave / S::WN) * S::TM + 16 * m + 4 * (lane >> 4);
+    const int col = tj * S::BN + (wave % S::WN) * S::TN + 16 * n + (lane & 15);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (row + v < p.M && col < p.N) {
+        float* o = p.out + (row + v) * p.ldo + col;
+        *o = p.accumulate ? *o + sum[i][v] : sum[i][v];
+      }
+  }
+}
 
 }  // namespace
-
-hipError_t launch_xent_counts(uint32_t* count, hipStream_t st) {
-  static_assert(kTileSlots256 <= 512, "one counter per thread");
-  k_f32_counts<<<dim3(1), dim3(512), 0, st>>>(count);
-  return hipGetLastError();
-}
 
 hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 kind, hipStream_t st) {
   const dim3 grid(p.items), block(512);
@@ -104,6 +135,9 @@ hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 
     case kXentDx32: k_f32_mm<kDx, false><<<grid, block, 0, st>>>(p, e); break;
     default: k_f32_mm<kDw, false><<<grid, block, 0, st>>>(p, e); break;
   }
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !p.apart) return err;
+  k_f32_join<<<dim3(8 * (p.tx * p.ty - p.full)), block, 0, st>>>(p);
   return hipGetLastError();
 }
 

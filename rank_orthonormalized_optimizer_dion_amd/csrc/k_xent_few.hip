@@ -1,4 +1,4 @@
-// Cross entropy of few tokens (up to 64): reading
+// Cross entropy of few tokens (at most 64): reading
 // W once per product, and writing dW, is what it costs, in any type and at any
 // alignment.  All products run on the bfloat16 matrix cores with operands that
 // come straight from global memory into registers:
@@ -160,14 +160,13 @@ __device__ __forceinline__ void prep_block(const XentPrep& a, int block, float* 
 
 template <bool F32>
 __global__ __launch_bounds__(512) void k_few_prep(XentPrep a) {
-  __shared__ float tile[64 * (kXentFew + 1)];
+  __shared__ float tile[64 * (kXentFewCopied + 1)];
   prep_block<F32>(a, blockIdx.x, tile);
 }
 
 // z for 16 RT rows of W at a time, its statistics or dz; the 8 wavefronts of a
 // workgroup take turns at 64-element pieces of the reduction.  What is read
-// again and again is x: RT blocks of rows share its operands (24 tokens, 2048
-// -> 32000 in bfloat16: @@).  RAW: x is read as it is, like W (one block of 16
+// again and again is x: RT blocks of rows share its operands.  RAW: x is read as it is, like W (one block of 16
 // tokens), else from planes whose rows are readable, and zero past k, up to f.kx
 // columns.  With dz, workgroups past the first `prep.first` transpose x for dW.
 template <int TB, int RT, bool F32, bool RAW, bool GRAD>
@@ -534,7 +533,7 @@ hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool 
 template <int TB, bool F32>
 hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int rt, int groups, hipStream_t st) {
   if (rt == 1) return few_z<TB, 1, F32>(f, e, prep, grad, raw, groups, st);
-  return few_z<TB, F32 && TB == 4 ? 2 : 4, F32>(f, e, prep, grad, raw, groups, st);
+  return few_z<TB, 4, F32>(f, e, prep, grad, raw, groups, st);
 }
 
 template <int TB, bool F32>
@@ -557,12 +556,11 @@ hipError_t few_dw(const XentFew& f, XentDw d, const XentDxSum& sum, hipStream_t 
 
 }  // namespace
 
-int few_rows(int t, bool f32, int64_t n) {
+int few_rows(int t, int64_t n) {
   // 64 rows of W per workgroup where that still makes one per CU: x is read a
   // quarter as often (24 tokens, 2048 -> 32000: 36 us, 55 with 16 rows; one
   // token, whose lanes read the same row of x: 34 us, 30 with 16)
-  const int rt = f32 && t > 32 ? 2 : 4;
-  return t > 4 && n >= 256 * 16 * rt ? rt : 1;
+  return t > 4 && n >= 256 * 64 ? 4 : 1;
 }
 
 hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st) {
@@ -576,8 +574,7 @@ hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep
                         int groups, hipStream_t st) {
   if (f32) {
     if (f.t <= 16) return few_z<1, true>(f, e, prep, grad, raw, rt, groups, st);
-    if (f.t <= 32) return few_z<2, true>(f, e, prep, grad, raw, rt, groups, st);
-    return few_z<4, true>(f, e, prep, grad, raw, rt, groups, st);
+    return few_z<2, true>(f, e, prep, grad, raw, rt, groups, st);
   }
   if (f.t <= 16) return few_z<1, false>(f, e, prep, grad, raw, rt, groups, st);
   return f.t <= 32 ? few_z<2, false>(f, e, prep, grad, raw, rt, groups, st)
@@ -587,8 +584,7 @@ hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep
 hipError_t launch_few_dx(const XentFew& f, const XentEpi& e, bool f32, int parts, float* part, hipStream_t st) {
   if (f32) {
     if (f.t <= 16) return few_dx<1, true>(f, e, parts, part, st);
-    if (f.t <= 32) return few_dx<2, true>(f, e, parts, part, st);
-    return few_dx<4, true>(f, e, parts, part, st);
+    return few_dx<2, true>(f, e, parts, part, st);
   }
   if (f.t <= 16) return few_dx<1, false>(f, e, parts, part, st);
   return f.t <= 32 ? few_dx<2, false>(f, e, parts, part, st) : few_dx<4, false>(f, e, parts, part, st);
@@ -600,9 +596,7 @@ hipError_t launch_few_dxsum(const XentDxSum& s, hipStream_t st) {
 }
 
 hipError_t launch_few_dw(const XentFew& f, const XentDw& d, const XentDxSum& sum, bool f32, hipStream_t st) {
-  if (f32) {
-    return f.tp <= 32 ? few_dw<1, true>(f, d, sum, st) : few_dw<2, true>(f, d, sum, st);
-  }
+  if (f32) return few_dw<1, true>(f, d, sum, st);
   return f.tp <= 32 ? few_dw<1, false>(f, d, sum, st) : few_dw<2, false>(f, d, sum, st);
 }
 

@@ -123,8 +123,9 @@ struct Product {
   LinKind kind;
   int tile;
 };
+// tile: 128 or 256, or 0 for the linear layer's rule.
 Product lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, bool padded,
-                    int nseg, LinKind kind, const LinOut& out) {
+                    int nseg, LinKind kind, const LinOut& out, int tile = 0) {
   Product f{};
   LinProduct& p = f.p;
   f.kind = kind;
@@ -141,7 +142,7 @@ Product lin_product(Run& r, const Operand& a, const Operand& b, int64_t M, int64
   p.nseg = nseg;
   p.out = out;
   // 256 x 256 tiles where they fill the chip
-  f.tile = lin_cdiv(M, 256) * lin_cdiv(N, 256) >= kLinBigTiles ? 256 : 128;
+  f.tile = tile ? tile : lin_cdiv(M, 256) * lin_cdiv(N, 256) >= kLinBigTiles ? 256 : 128;
   p.tx = static_cast<int32_t>(lin_cdiv(M, f.tile));
   p.ty = static_cast<int32_t>(lin_cdiv(N, f.tile));
   const Cut16 c = cut_tiles(static_cast<int64_t>(p.tx) * p.ty, f.tile, lin_cdiv(K, kLinStage) * nseg);

@@ -84,25 +84,40 @@ int64_t xent_piece(int64_t n, int64_t row) {
 
 // Few tokens: their own kernels (k_xent_few.hip).
 bool xent_few(const XentCall& c) {
-  return c.a.t <= (lin_direct(c.x) && lin_direct(c.w) ? kXentFewDirect : kXentFew);
+  const bool copied = c.e == 2 && !(lin_direct(c.x) && lin_direct(c.w));
+  return c.a.t <= (copied ? kXentFewCopied : kXentFew);
 }
 
-// The products of one piece or call, after the copies that they need; the
-// copies and counters of the launch are then done.
+// A call's copies, counters and workspace.
 struct XentRun : Run {
   size_t peak = 0;
-  hipError_t packs() {
-    if (!this->go || (this->Run::packs.n == 0 && this->Run::packs.counts == 0)) return hipSuccess;
-    return launch_lin_packs(this->Run::packs, st);
+  XentCopies copies{};
+  int copied = 0;
+  // A bfloat16 operand, in place or as a copy in the next launch of copies.
+  void operand(const Span& s, Operand& out) {
+    if (lin_direct(s)) {
+      out = {static_cast<const uint16_t*>(s.p), s.ld, 0};
+      return;
+    }
+    XentCopy& c = copies.c[copied++];
+    c.src = static_cast<const uint16_t*>(s.p);
+    c.ld = s.ld;
+    c.rows = s.rows;
+    c.prows = lin_cdiv(s.rows, kLinStage) * kLinStage;
+    c.cols = static_cast<int32_t>(s.cols);
+    c.pitch = lin_cdiv(s.cols, 64) * 64;
+    c.dst = ws.take<uint16_t>(c.prows * c.pitch);
+    out = {c.dst, c.pitch, 0};
   }
-  hipError_t counts32() {   // the counters of a call's cut tiles, once
-    if (!this->go || this->Run::packs.counts == 0) return hipSuccess;
-    return launch_xent_counts(this->Run::packs.count, st);
-  }
-  void done() {
+  // The copies (and counters) that the products to come need.
+  hipError_t prepare() {
+    copies.count = packs.counts > 0 ? packs.count : nullptr;
+    const hipError_t e = go && (copied > 0 || copies.count) ? launch_xent_copies(copies, st) : hipSuccess;
     peak = std::max(peak, ws.used);
-    Run::packs.n = 0;
-    Run::packs.counts = 0;
+    copies = {};
+    copied = 0;
+    packs.counts = 0;
+    return e;
   }
 };
 
@@ -147,10 +162,34 @@ XentPrep few_prep(XentRun& r, const XentCall& c, bool planes, bool transposed, X
 // of rows in turn.
 int64_t few_groups(int64_t n, int rt) { return std::min<int64_t>(lin_cdiv(n, 16 * rt), 1024); }
 
+// The size of a bfloat16 product's tiles by its estimated time, in stages of a
+// 256 x 256 tile (0.9 us): rounds of whole tiles, a cut round, a tile's first
+// loads and epilogue (6 or 4), and the join of a cut round, whose sums all go
+// through memory (18 or 9) before one workgroup per tile reads its slices (2.2
+// or 0.6 each).  A stage of a 128 x 128 tile, two of which share a CU, takes
+// 0.65.  Against both sizes timed over 30 products (65 to 8192 tokens, widths of
+// 512 to 4096, 5000 to 128000 words) it takes the faster one, or one within 3% of
+// it; the linear layer's rule (256 tiles of 256 x 256) took the other one in
+// four: dx of 2048 tokens, 4096 -> 32000, 616 us against 453.
+double xent_estimate(int64_t M, int64_t N, int64_t K, int tile) {
+  const int64_t stages = lin_cdiv(K, kLinStage);
+  const Cut16 c = cut_tiles(lin_cdiv(M, tile) * lin_cdiv(N, tile), tile, stages);
+  const bool big = tile == 256;
+  // tiles that cut_tiles leaves whole in the last round are counted as a round
+  const int64_t rounds = lin_cdiv(c.full, tile_slots(tile)), last = c.cut > 0;
+  const double step = big ? 1.0 : 0.65, start = big ? 6.0 : 4.0;
+  double t = (rounds + last) * start + (rounds + (last ? 1.0 / c.slices : 0.0)) * stages * step;
+  if (last && c.slices > 1) t += big ? 18.0 + 2.2 * c.slices : 9.0 + 0.6 * c.slices;
+  return t;
+}
+int xent_tile(int64_t M, int64_t N, int64_t K) {
+  return xent_estimate(M, N, K, 256) <= xent_estimate(M, N, K, 128) ? 256 : 128;
+}
+
 // One float32 product, cut along long reductions as the other tiles are: a
 // stage is six products of half a 256 x 256 tile.
 XentProduct32 xent_product32(XentRun& r, const float* A, int64_t lda, const float* B, int64_t ldb, int64_t M, int64_t N,
-                             int64_t K) {
+                             int64_t K, bool gradient) {
   XentProduct32 p{};
   p.a = A;
   p.b = B;
@@ -167,9 +206,10 @@ XentProduct32 xent_product32(XentRun& r, const float* A, int64_t lda, const floa
   p.slices = static_cast<int32_t>(c.slices);
   if (c.cut) {
     p.part = r.ws.take<float>(c.cut * c.slices * kXentM32 * kXentN32);
-    p.count = r.Run::packs.count;
-    r.Run::packs.counts = 1;
+    p.count = r.packs.count;
+    r.packs.counts = 1;
   }
+  p.apart = gradient && c.cut && c.slices >= kXentApart;
   return p;
 }
 
@@ -182,7 +222,7 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const bool copy = !few && !f32 && !lin_direct(c.w);
   const int64_t piece = copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n;
   // one partial column per 64 columns at least
-  const int rt = few_rows(static_cast<int>(a.t), c.e == 4, a.n);
+  const int rt = few_rows(static_cast<int>(a.t), a.n);
   const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4 * lin_cdiv(a.n, piece);
   XentEpi e{};
   e.target = a.target;
@@ -202,27 +242,26 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
     if (r.go) LIN_TRY(launch_few_z(f, e, prep, c.e == 4, false, raw, rt, static_cast<int>(cols), r.st));
   } else if (f32) {
     const XentProduct32 z = xent_product32(r, static_cast<const float*>(a.x), a.ldx, static_cast<const float*>(a.w), a.ldw,
-                                           a.t, a.n, a.k);
+                                           a.t, a.n, a.k, false);
     cols = xent_tile_cols32(z.ty);
-    LIN_TRY(r.counts32());
+    LIN_TRY(r.prepare());
     if (r.go) LIN_TRY(launch_xent_f32(z, e, kXentStats32, r.st));
   } else {
     Operand x;
-    lin_operand(r, c.x, x);
+    r.operand(c.x, x);
     const size_t mark = r.ws.used;
     for (int64_t j0 = 0; j0 < a.n; j0 += piece) {
       r.ws.used = mark;
       const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
       Operand w;
-      lin_operand(r, wj, w);
+      r.operand(wj, w);
       const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, !lin_direct(c.x) && !lin_direct(c.w), 1, kLinForward,
-                                    LinOut{});
+                                    LinOut{}, xent_tile(a.t, wj.rows, a.k));
       e.j0 = static_cast<int32_t>(j0);
       e.col0 = static_cast<int32_t>(cols);
       cols += xent_tile_cols(z.p.ty);
-      LIN_TRY(r.packs());
+      LIN_TRY(r.prepare());
       if (r.go) LIN_TRY(launch_xent_product(z.p, e, false, z.tile, r.st));
-      r.done();
     }
   }
   if (!r.go) return hipSuccess;
@@ -276,7 +315,7 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
     f.w = wj.p;
     f.n = static_cast<int32_t>(wj.rows);
     e.j0 = static_cast<int32_t>(j0);
-    const int rt = few_rows(f.t, f32, e.pitch);
+    const int rt = few_rows(f.t, e.pitch);
     prep.first = static_cast<int32_t>(few_groups(e.pitch, rt));
     LIN_TRY(launch_few_z(f, e, prep, f32, true, false, rt, 0, r.st));
     prep.xt = nullptr;
@@ -307,28 +346,27 @@ hipError_t xent_backward_f32(XentRun& r, const XentCall& c) {
     r.ws.used = mark;
     const int64_t n = std::min(piece, a.n - j0);
     const float* w = static_cast<const float*>(xent_rows(c.w, j0, n).p);
-    const XentProduct32 z = xent_product32(r, x, a.ldx, w, a.ldw, a.t, n, a.k);
+    const XentProduct32 z = xent_product32(r, x, a.ldx, w, a.ldw, a.t, n, a.k, false);
     XentProduct32 dx{}, dw{};
     if (a.dx) {
-      dx = xent_product32(r, e.dz32, e.pitch, w, a.ldw, a.t, a.k, n);
+      dx = xent_product32(r, e.dz32, e.pitch, w, a.ldw, a.t, a.k, n, true);
       dx.out = static_cast<float*>(a.dx);
       dx.ldo = a.lddx;
       dx.accumulate = j0 > 0;
     }
     if (a.dw) {
-      dw = xent_product32(r, e.dz32, e.pitch, x, a.ldx, n, a.k, a.t);
+      dw = xent_product32(r, e.dz32, e.pitch, x, a.ldx, n, a.k, a.t, true);
       dw.out = static_cast<float*>(const_cast<void*>(xent_rows(c.dw, j0, n).p));
       dw.ldo = a.lddw;
       dw.accumulate = a.accumulate != 0;
     }
     e.j0 = static_cast<int32_t>(j0);
-    if (j0 == 0) LIN_TRY(r.counts32());   // every launch leaves them cleared
+    LIN_TRY(r.prepare());
     if (r.go) {
       LIN_TRY(launch_xent_f32(z, e, kXentDz32, r.st));
       if (a.dx) LIN_TRY(launch_xent_f32(dx, e, kXentDx32, r.st));
       if (a.dw) LIN_TRY(launch_xent_f32(dw, e, kXentDw32, r.st));
     }
-    r.peak = std::max(r.peak, r.ws.used);
   }
   return hipSuccess;
 }
@@ -347,7 +385,7 @@ hipError_t xent_backward_bf16(XentRun& r, const XentCall& c) {
   const bool sum = a.dx && piece < a.n;
   float* dxsum = sum ? r.ws.take<float>(a.t * a.k) : nullptr;
   Operand x{};
-  lin_operand(r, c.x, x);
+  r.operand(c.x, x);
   const bool padded = !lin_direct(c.w), xpadded = !lin_direct(c.x);
   const size_t mark = r.ws.used;
   for (int64_t j0 = 0; j0 < a.n; j0 += piece) {
@@ -355,9 +393,10 @@ hipError_t xent_backward_bf16(XentRun& r, const XentCall& c) {
     const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
     const bool last = j0 + piece >= a.n;
     Operand w{};
-    lin_operand(r, wj, w);
+    r.operand(wj, w);
     Product dx{}, dw{};
-    const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, padded && xpadded, 1, kLinForward, LinOut{});
+    const Product z = lin_product(r, x, w, a.t, wj.rows, a.k, padded && xpadded, 1, kLinForward, LinOut{},
+                                  xent_tile(a.t, wj.rows, a.k));
     if (a.dx) {
       LinOut o = out;
       o.y = a.dx;
@@ -373,7 +412,7 @@ hipError_t xent_backward_bf16(XentRun& r, const XentCall& c) {
         o.ldr = a.k;
         o.wide = 1;
       }
-      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, padded, 1, kLinDx, o);
+      dx = lin_product(r, dz, w, a.t, a.k, wj.rows, padded, 1, kLinDx, o, xent_tile(a.t, a.k, wj.rows));
     }
     if (a.dw) {
       LinOut o = out;
@@ -381,16 +420,15 @@ hipError_t xent_backward_bf16(XentRun& r, const XentCall& c) {
       o.y = const_cast<void*>(dj.p);
       o.ldy = a.lddw;
       o.accumulate = a.accumulate != 0;
-      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, xpadded, 1, kLinDw, o);
+      dw = lin_product(r, dz, x, wj.rows, a.k, a.t, xpadded, 1, kLinDw, o, xent_tile(wj.rows, a.k, a.t));
     }
     e.j0 = static_cast<int32_t>(j0);
-    LIN_TRY(r.packs());
+    LIN_TRY(r.prepare());
     if (r.go) {
       LIN_TRY(launch_xent_product(z.p, e, true, z.tile, r.st));
       if (a.dx) LIN_TRY(launch_lin_product(dx.p, kLinDx, dx.tile, r.st));
       if (a.dw) LIN_TRY(launch_lin_product(dw.p, kLinDw, dw.tile, r.st));
     }
-    r.done();
   }
   return hipSuccess;
 }
@@ -406,7 +444,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
     out.y = a.dw;
     out.ldy = a.lddw;
     const Product dw = lin_product(r, Operand{}, Operand{}, a.n, a.k, 0, false, 1, kLinDw, out);
-    LIN_TRY(r.packs());
+    LIN_TRY(r.prepare());
     return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
   }
   if (xent_few(c)) return xent_backward_few(r, c);
@@ -415,9 +453,9 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
 
 template <class Go>
 hipError_t xent_go(XentRun& r, const XentCall& c, Go go) {
-  r.Run::packs.count = r.ws.take<uint32_t>(kTileSlots128);
+  r.packs.count = r.ws.take<uint32_t>(kTileSlots128);
   const hipError_t e = go(r, c);
-  r.done();
+  r.peak = std::max(r.peak, r.ws.used);
   return e;
 }
 

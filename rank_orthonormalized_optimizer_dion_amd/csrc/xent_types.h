@@ -64,16 +64,21 @@ struct XentProduct32 {
   float* out;              // dx, dW
   int64_t ldo;
   int32_t accumulate;
+  int32_t apart;           // dx, dW: cut tiles are added up by a launch of their own
 };
+// Cut tiles of at least this many slices, which one workgroup per tile would
+// read one after the other.
+constexpr int kXentApart = 6;
 enum XentKind32 { kXentStats32 = 0, kXentDz32, kXentDx32, kXentDw32 };
 hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 kind, hipStream_t st);
-hipError_t launch_xent_counts(uint32_t* count, hipStream_t st);   // clears kTileSlots256
 
 // Few tokens (k_xent_few.hip).
-// tokens; with a bfloat16 x and W of whole 16-byte pieces, which the tiles read
-// in place, half as many (2048 -> 32000, gradients: 32 tokens 114 us, 64 tokens
-// 163 and as tiles 151; 768 -> 50257: 64 tokens 148, as tiles 113)
-constexpr int kXentFew = 64, kXentFewDirect = 32;
+// Tokens: up to 64 in bfloat16 where the tiles would need copies of x or W (2048
+// -> 32000 at an odd pitch, 64 tokens, gradients: 224 us, 65 as tiles 299), up
+// to 32 where they read them in place (32 tokens, gradients: 114 us, 40 as tiles
+// 141; 64 tokens 163 and 143) and in float32 (24 tokens: 78 us forward, 65 as tiles
+// 100, 64 of them 159).
+constexpr int kXentFewCopied = 64, kXentFew = 32;
 constexpr int kFewDwRows = 64;     // rows of dW of a wavefront
 struct XentFew {
   const void* w;           // n rows of k
@@ -113,7 +118,7 @@ struct XentDxSum {
   int32_t dtype;
 };
 // Blocks of 16 rows of W that a workgroup turns into z at a time.
-int few_rows(int t, bool f32, int64_t n);
+int few_rows(int t, int64_t n);
 // raw: x as it is (at most 16 tokens, no grad); groups: forward's workgroups,
 // each of which leaves one partial column; prep (grad): first, and xt or null
 hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool f32, bool grad, bool raw, int rt,
@@ -122,6 +127,23 @@ hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st);
 hipError_t launch_few_dx(const XentFew& f, const XentEpi& e, bool f32, int parts, float* part, hipStream_t st);
 hipError_t launch_few_dxsum(const XentDxSum& s, hipStream_t st);
 hipError_t launch_few_dw(const XentFew& f, const XentDw& d, const XentDxSum& sum, bool f32, hipStream_t st);
+
+// bfloat16 operands in a layout that the tiles read (rows x cols of pitch ld, to
+// prows x pitch), and the cut tiles' arrival counters cleared.
+struct XentCopy {
+  const uint16_t* src;
+  int64_t ld;
+  int64_t rows, prows;
+  int32_t cols;
+  uint16_t* dst;
+  int64_t pitch;
+  int32_t blocks;          // set at the launch
+};
+struct XentCopies {
+  XentCopy c[2];
+  uint32_t* count;         // or null
+};
+hipError_t launch_xent_copies(XentCopies a, hipStream_t st);
 
 // z by tiles; grad: backward.
 hipError_t launch_xent_product(const LinProduct& p, const XentEpi& e, bool grad, int tile, hipStream_t st);

@@ -1,5 +1,5 @@
-"""The cross entropy of few tokens (GPU): its own kernels up to 64 tokens (32
-where the tiles can read x and W in place), on both sides of each of their block
+"""The cross entropy of few tokens (GPU): its own kernels up to 32 tokens (64
+where the tiles would need copies of x and W), on both sides of each of their block
 sizes, at every alignment, with short and long vocabularies and reductions.
 Same checks and tolerances as the other sizes."""
 import pytest
