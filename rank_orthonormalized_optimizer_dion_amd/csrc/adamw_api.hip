@@ -70,17 +70,20 @@ int adamw_run(const dion_adamw_tensor* list, int count, double lr, double beta1,
     elements += list[i].n;
   }
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const int quads = elements > (int64_t{1} << 20) ? 4 : 1;
+  // bytes read and written per element
+  const int64_t each = 8 + (gdtype == DION_DTYPE_BF16 ? 2 : 4) + (state_bits == DION_STATE_8BIT ? 4 : 16);
+  const bool large = elements > kAdamwLarge / each;
+  const int64_t chunk = 1024 * adamw_quads(state_bits, large);
   const auto flush = [&] {
     if (L.count == 0) return hipSuccess;
-    const hipError_t e = launch_adamw(L, gdtype, state_bits, quads, st);
+    const hipError_t e = launch_adamw(L, gdtype, state_bits, large, st);
     L.count = L.total = 0;
     return e;
   };
   for (int i = 0; i < count; ++i) {
     const dion_adamw_tensor& a = list[i];
     if (a.n == 0) continue;
-    const int64_t items = (a.n + adamw_chunk(quads) - 1) / adamw_chunk(quads);
+    const int64_t items = (a.n + chunk - 1) / chunk;
     if (L.count == kAdamwTensors || items > INT32_MAX - L.total)
       if (flush() != hipSuccess) return DION_ERR_HIP;
     const int se = state_bits == DION_STATE_8BIT ? 4 : 16;   // bytes of four elements' states

@@ -39,9 +39,13 @@ struct AdamwLaunch {
 constexpr int kAdamwTensors = 72, kAdamwFew = 4;
 static_assert(sizeof(AdamwLaunch<kAdamwTensors>) <= 4096, "kernel arguments");
 
-// Elements of a workgroup of 256 threads: `quads` times four per thread.
-inline int64_t adamw_chunk(int quads) { return 1024 * static_cast<int64_t>(quads); }
-// quads: 1 or 4
-hipError_t launch_adamw(const AdamwLaunch<kAdamwTensors>& L, int gdtype, int state_bits, int quads, hipStream_t st);
+// Steps that move more than the memory-side cache holds go past the caches: 40
+// million elements 176 us, through them 192; 10 million 43 and 40.
+constexpr int64_t kAdamwLarge = int64_t{256} << 20;
+// Pieces of four elements per thread, 256 threads per workgroup: two in large
+// steps with 8-bit states (40 million elements 109 us, 114 with one), else one
+// (float32: 176, with two 176, with four 180).
+constexpr __host__ __device__ int adamw_quads(int state_bits, bool large) { return state_bits == 8 && large ? 2 : 1; }
+hipError_t launch_adamw(const AdamwLaunch<kAdamwTensors>& L, int gdtype, int state_bits, bool large, hipStream_t st);
 
 }  // namespace dion

@@ -186,10 +186,13 @@ def test_lists_and_alignment(gpu_lib, gdt, bits, shift):
 
 @pytest.mark.parametrize("bits", [32, 8])
 def test_large_launches(gpu_lib, bits):
-    """Past 2^20 elements a thread takes four pieces."""
+    """Several workgroups per tensor; past 256 MiB the accesses go past the
+    caches, in other pieces."""
     say(f"adamw large {bits}")
     run(gpu_lib, [1 << 20, 70001, 64, 1 << 18], "bfloat16", bits)
     run(gpu_lib, [3000017], "float32", bits, shift=1, steps=1)
+    run(gpu_lib, [9000001, 77, 12000003, 1025], "bfloat16", bits, steps=1)
+    run(gpu_lib, [20000001, 2], "float32", bits, shift=2, steps=1)
 
 
 @pytest.mark.parametrize("bits", [32, 8])
