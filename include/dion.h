@@ -466,10 +466,10 @@ int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace
  * sums in float32; dz is rounded to bfloat16 before its two products (to 16
  * bits with at most 32 tokens, to 24 in float32) and computed a piece of the
  * vocabulary at a time, so that the workspace stays near 256 MiB plus, in
- * bfloat16, t x k float32 where there are several pieces, plus copies of
- * operands that the tiles cannot read in place.  Forward keeps at most an eighth
- * of a byte per logit (one and a half times that with label smoothing), few
- * tokens up to half a byte.
+ * bfloat16, t x k float32 where there are several pieces and copies of operands
+ * that the tiles cannot read in place.  Forward keeps at most an eighth of a
+ * byte per logit (one and a half times that with label smoothing), few tokens up
+ * to half a byte, and such copies, of W a piece at a time.
  *
  * Forward reads x, w, target and writes those of loss and lse that are not
  * NULL.  Backward reads x, w, target, lse (forward's) and dloss and writes
@@ -532,12 +532,15 @@ int dion_cross_entropy_backward(const dion_cross_entropy* a, void* workspace, si
  *     A block with a new m or v that is not finite becomes NaN as a whole.
  *
  * Everything else that is not finite reaches the elements it belongs to.
- * Tensors of a list share no memory; X, M, V, S and G of one do not overlap.
- * Pointers in their elements' alignment (16 bytes are faster), 0 <= n <= 2^36
+ * Tensors of a list share no memory; X, M, V, S and G of one do not overlap, and
+ * X, M, V and S do not hold grad_scale.
+ * Pointers in their elements' alignment (16 bytes are faster), 0 <= n <= 2^33
  * (n = 0: pointers are not looked at), float32 X, G of one type for the list, at
  * most DION_MAX_LIST tensors.  0 <= beta1, beta2 < 1; lr, weight_decay finite;
- * 1.2e-38 <= eps <= 1e30.  The list is read before the call returns; no
- * workspace; the same call gives the same bits. */
+ * 1.2e-38 <= eps <= 1e30.  The list is read before the call returns, and with
+ * lr, step and seed is part of what a stream capture records: only c and the
+ * tensors can change from replay to replay.  No workspace; the same call gives
+ * the same bits. */
 #define DION_STATE_F32   32
 #define DION_STATE_8BIT  8
 #define DION_ADAMW_BLOCK 64

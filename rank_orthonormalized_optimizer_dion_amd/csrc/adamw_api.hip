@@ -15,7 +15,9 @@ static_assert(dion::kAdamwBlock == DION_ADAMW_BLOCK, "block of the 8-bit states"
 namespace dion {
 namespace {
 
-constexpr int64_t kAdamwMaxElements = int64_t{1} << 36;
+constexpr int64_t kAdamwMaxElements = int64_t{1} << 33;
+constexpr int32_t kAdamwMaxItems = (1 << 24) - 1;   // of a launch: fewer than 2^32 threads
+static_assert(kAdamwMaxElements / 1024 <= kAdamwMaxItems, "a tensor fits a launch");
 
 struct Bytes {
   uintptr_t p;
@@ -23,7 +25,7 @@ struct Bytes {
 };
 bool bytes_overlap(const Bytes& a, const Bytes& b) { return a.p < b.p + b.n && b.p < a.p + a.n; }
 
-bool adamw_ok(const dion_adamw_tensor& t, int gdtype, int state_bits) {
+bool adamw_ok(const dion_adamw_tensor& t, int gdtype, int state_bits, const float* grad_scale) {
   if (t.n < 0 || t.n > kAdamwMaxElements || !std::isfinite(t.weight_decay)) return false;
   if (t.n == 0) return true;
   const bool eight = state_bits == DION_STATE_8BIT;
@@ -35,9 +37,12 @@ bool adamw_ok(const dion_adamw_tensor& t, int gdtype, int state_bits) {
                        {reinterpret_cast<uintptr_t>(eight ? t.S : nullptr), eight ? 2 * ((n + kAdamwBlock - 1) / kAdamwBlock) : 0},
                        {reinterpret_cast<uintptr_t>(t.G), ge * n}};
   if (all[0].p % 4 != 0 || all[1].p % se != 0 || all[2].p % se != 0 || all[4].p % ge != 0) return false;
-  for (int i = 0; i < 5; ++i)
+  const Bytes scale = {reinterpret_cast<uintptr_t>(grad_scale), 4};
+  for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < i; ++j)
       if (all[i].n && all[j].n && bytes_overlap(all[i], all[j])) return false;
+    if (i < 4 && grad_scale && all[i].n && bytes_overlap(all[i], scale)) return false;   // G may hold it
+  }
   return true;
 }
 
@@ -65,7 +70,7 @@ int adamw_run(const dion_adamw_tensor* list, int count, double lr, double beta1,
   if (!std::isfinite(L.rate) || !std::isfinite(L.root)) return DION_ERR_INVALID_ARG;
   int64_t elements = 0;
   for (int i = 0; i < count; ++i) {
-    if (!adamw_ok(list[i], gdtype, state_bits)) return DION_ERR_INVALID_ARG;
+    if (!adamw_ok(list[i], gdtype, state_bits, grad_scale)) return DION_ERR_INVALID_ARG;
     if (!std::isfinite(static_cast<float>(1.0 - lr * list[i].weight_decay))) return DION_ERR_INVALID_ARG;
     elements += list[i].n;
   }
@@ -84,7 +89,7 @@ int adamw_run(const dion_adamw_tensor* list, int count, double lr, double beta1,
     const dion_adamw_tensor& a = list[i];
     if (a.n == 0) continue;
     const int64_t items = (a.n + chunk - 1) / chunk;
-    if (L.count == kAdamwTensors || items > INT32_MAX - L.total)
+    if (L.count == kAdamwTensors || items > kAdamwMaxItems - L.total)
       if (flush() != hipSuccess) return DION_ERR_HIP;
     const int se = state_bits == DION_STATE_8BIT ? 4 : 16;   // bytes of four elements' states
     const bool vec = aligned(a.X, 16) && aligned(a.G, gdtype == DION_DTYPE_BF16 ? 8 : 16) && aligned(a.M, se) && aligned(a.V, se);

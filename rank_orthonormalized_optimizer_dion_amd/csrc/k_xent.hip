@@ -114,7 +114,8 @@ __global__ __launch_bounds__(256) void k_xent_join(XentJoin j) {
 
 // Copies of bfloat16 operands whose rows the tiles cannot read in place: 16
 // bytes per thread and step, zero past the columns and (to the last whole
-// stage) past the rows.  32000 x 1999: @@.
+// stage) past the rows.  65 tokens, 1999 -> 32000, forward: 168 us with the
+// linear layer's copies, 2 bytes per access, 92 with these.
 __global__ __launch_bounds__(256) void k_xent_copy(XentCopies a) {
   const int which = static_cast<int>(blockIdx.x) >= a.c[0].blocks;
   const XentCopy c = a.c[which];

@@ -218,9 +218,11 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   if (a.t == 0) return hipSuccess;
   const bool few = xent_few(c);
   const bool f32 = !few && c.e == 4;
-  // a piece at a time only where W has to be copied
+  // a piece at a time where W has to be copied, and where one launch would have
+  // more threads than a grid can (2^32: 2^22 tiles of 128 x 128, far fewer of others)
   const bool copy = !few && !f32 && !lin_direct(c.w);
-  const int64_t piece = copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n;
+  const int64_t most_cols = few ? a.n : std::max(kXentStep, (int64_t{1} << 22) / lin_cdiv(a.t, 128) * 128 / kXentStep * kXentStep);
+  const int64_t piece = std::min(most_cols, copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n);
   // one partial column per 64 columns at least
   const int rt = few_rows(static_cast<int>(a.t), a.n);
   const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4 * lin_cdiv(a.n, piece);
@@ -241,11 +243,18 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
     if (r.go && prep.xp) LIN_TRY(launch_few_prep(prep, c.e == 4, r.st));
     if (r.go) LIN_TRY(launch_few_z(f, e, prep, c.e == 4, false, raw, rt, static_cast<int>(cols), r.st));
   } else if (f32) {
-    const XentProduct32 z = xent_product32(r, static_cast<const float*>(a.x), a.ldx, static_cast<const float*>(a.w), a.ldw,
-                                           a.t, a.n, a.k, false);
-    cols = xent_tile_cols32(z.ty);
-    LIN_TRY(r.prepare());
-    if (r.go) LIN_TRY(launch_xent_f32(z, e, kXentStats32, r.st));
+    const size_t mark = r.ws.used;
+    for (int64_t j0 = 0; j0 < a.n; j0 += piece) {
+      r.ws.used = mark;
+      const Span wj = xent_rows(c.w, j0, std::min(piece, a.n - j0));
+      const XentProduct32 z = xent_product32(r, static_cast<const float*>(a.x), a.ldx, static_cast<const float*>(wj.p), a.ldw,
+                                             a.t, wj.rows, a.k, false);
+      e.j0 = static_cast<int32_t>(j0);
+      e.col0 = static_cast<int32_t>(cols);
+      cols += xent_tile_cols32(z.ty);
+      LIN_TRY(r.prepare());
+      if (r.go) LIN_TRY(launch_xent_f32(z, e, kXentStats32, r.st));
+    }
   } else {
     Operand x;
     r.operand(c.x, x);

@@ -29,9 +29,10 @@ def call(lib, count=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, c=None, bits
     dict(step=-3), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=math.nan), dict(lr=math.inf), dict(lr=math.nan),
     dict(eps=0.0), dict(eps=-1e-8), dict(eps=math.inf), dict(eps=1e-39), dict(weight_decay=math.nan),
     dict(lr=1e30, weight_decay=1e30), dict(lr=1e300, b1=0.5), dict(c=C + 2),
-    dict(n=-1), dict(n=(1 << 36) + 1), dict(n=8, X=None), dict(n=8, G=None), dict(n=8, M=None), dict(n=8, V=None),
+    dict(n=-1), dict(n=(1 << 33) + 1), dict(n=8, X=None), dict(n=8, G=None), dict(n=8, M=None), dict(n=8, V=None),
     dict(n=8, S=None, bits=8), dict(n=8, X=X + 2), dict(n=8, G=G + 2), dict(n=8, G=G + 1, gd=1), dict(n=8, M=M + 1),
     dict(n=8, V=V + 2), dict(n=8, G=X + 28), dict(n=8, M=X + 28), dict(n=8, V=M + 28), dict(n=8, V=G),
+    dict(n=8, c=X + 28), dict(n=8, c=M), dict(n=65, bits=8, c=S),
     dict(n=65, bits=8, S=M + 64), dict(n=65, bits=8, V=S + 3), dict(n=65, bits=8, S=X + 259),
 ])
 def test_refuses(lib, kw):

@@ -413,6 +413,24 @@ def test_offsets_past_32_bits(gpu_lib):
         assert float(torch.linalg.vector_norm(dx[a].double() - want) / torch.linalg.vector_norm(want)) < 2.0 ** -7
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_more_tiles_than_a_launch(gpu_lib, dtype):
+    """2^20 tokens on 65836 words: the forward pass takes the vocabulary in pieces."""
+    import torch
+    t, k, n = 1 << 20, 8, 65836
+    say("cross entropy, many tiles", t, k, n, dtype)
+    x, w, y, _ = inputs(t, k, n, dtype)
+    loss = torch.full((t,), float("nan"), device="cuda")
+    lse = torch.full_like(loss, float("nan"))
+    gpu_lib.cross_entropy_forward(x, w, y, loss, lse=lse, ignore_index=IGNORE)
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(lse).all())
+    some = torch.cat([torch.arange(0, t, 20011, device="cuda"), torch.arange(t - 5, t, device="cuda")])
+    dz = z_error(x[some], w) + 2.0 ** -21
+    eloss, else_ = reference(x[some], w, y[some], 0.0, 0.0)
+    assert bool(((lse[some].double() - else_).abs() <= dz + 2.0 ** -23 * (1 + else_.abs())).all())
+    assert bool(((loss[some].double() - eloss).abs() <= 2 * dz + 2.0 ** -22 * (1 + eloss.abs())).all())
+
+
 def test_binding_refuses(gpu_lib):
     import torch
     x, w, y, dloss = inputs(4, 16, 20, "float32")
