@@ -29,11 +29,16 @@ namespace dion {
 namespace {
 
 // 16 bytes at any alignment of the element type (global memory takes vector
-// accesses at any address).
-template <class V, class T>
+// accesses at any address).  FAR: past the caches.
+template <class V, bool FAR = false, class T>
 __device__ __forceinline__ V load_any(const T* p) {
   V v;
-  __builtin_memcpy(&v, p, sizeof(V));
+  if constexpr (FAR) {
+    typedef V Any __attribute__((aligned(2)));
+    v = __builtin_nontemporal_load(reinterpret_cast<const Any*>(p));
+  } else {
+    __builtin_memcpy(&v, p, sizeof(V));
+  }
   return v;
 }
 
@@ -79,7 +84,7 @@ template <bool F32>
 struct Raw16 {
   u32x4 v[F32 ? 4 : 2];
 };
-template <bool F32, bool TAIL>
+template <bool F32, bool TAIL, bool FAR = false>
 __device__ __forceinline__ Raw16<F32> load16(const void* row, int c, int k) {
   constexpr int N = F32 ? 4 : 8;   // elements of a load
   using T = typename std::conditional<F32, float, uint16_t>::type;
@@ -90,7 +95,7 @@ __device__ __forceinline__ Raw16<F32> load16(const void* row, int c, int k) {
     const int c0 = c + (F32 ? 16 : 32) * i + N * g;
     const T* p = static_cast<const T*>(row) + c0;
     if (!TAIL || c0 + N <= k) {
-      o.v[i] = load_any<u32x4>(p);
+      o.v[i] = load_any<u32x4, FAR>(p);
     } else {
       T v[N];
 #pragma unroll
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(512) void k_few_prep(XentPrep a) {
 // again and again is x: RT blocks of rows share its operands.  RAW: x is read as it is, like W (one block of 16
 // tokens), else from planes whose rows are readable, and zero past k, up to f.kx
 // columns.  With dz, workgroups past the first `prep.first` transpose x for dW.
-template <int TB, int RT, bool F32, bool RAW, bool GRAD>
+template <int TB, int RT, bool F32, bool RAW, bool GRAD, bool FAR>
 __global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e, XentPrep prep) {
   constexpr int P = F32 ? 3 : 1, ES = F32 ? 4 : 2;
   constexpr int B = (TB + 1) / 2;                       // 512 threads hold 32 tokens by 16 rows of W
@@ -228,7 +233,7 @@ __global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e, XentPrep pr
       for (int u = 0; u < N; ++u) {
         const int k = k0 + 512 * u;
 #pragma unroll
-        for (int q = 0; q < RT; ++q) w[u][q] = load16<F32, TAIL>(wr[q], k, f.k);
+        for (int q = 0; q < RT; ++q) w[u][q] = load16<F32, TAIL, FAR>(wr[q], k, f.k);
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
           if constexpr (RAW) {
@@ -329,7 +334,7 @@ __global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e, XentPrep pr
 
 // dx's sums over every `gridDim.y`-th block of 4 x 32 rows of W, for 16
 // times CW columns.
-template <int TB, bool F32>
+template <int TB, bool F32, bool FAR>
 __global__ __launch_bounds__(256, 2) void k_few_dx(XentFew f, const uint16_t* dz, int64_t pitch, int64_t plane, float* part) {
   constexpr int CW = F32 ? 4 : 8, PW = F32 ? 3 : 1, PZ = F32 ? 3 : 2;
   using T = typename std::conditional<F32, float, uint16_t>::type;
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(256, 2) void k_few_dx(XentFew f, const uint16_t* dz
     for (int i = 0; i < 8; ++i) {
       const T* p = static_cast<const T*>(f.w) + min(j0 + i, f.n - 1) * f.ldw + c;
       if (whole) {
-        w[i] = load_any<u32x4>(p);
+        w[i] = load_any<u32x4, FAR>(p);
       } else {
         T v[CW];
 #pragma unroll
@@ -517,29 +522,32 @@ __global__ __launch_bounds__(256, 2) void k_few_dw(XentFew f, XentDw d, XentDxSu
   }
 }
 
-template <int TB, int RT, bool F32>
+template <int TB, int RT, bool F32, bool FAR>
 hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int groups, hipStream_t st) {
   const dim3 grid(grad ? prep.first + (prep.xt ? (f.k + 63) / 64 : 0) : groups), block(512);
   if (grad) {
-    k_few_z<TB, RT, F32, false, true><<<grid, block, 0, st>>>(f, e, prep);
+    k_few_z<TB, RT, F32, false, true, FAR><<<grid, block, 0, st>>>(f, e, prep);
   } else if constexpr (TB == 1) {
-    if (raw) k_few_z<TB, RT, F32, true, false><<<grid, block, 0, st>>>(f, e, prep);
-    else k_few_z<TB, RT, F32, false, false><<<grid, block, 0, st>>>(f, e, prep);
+    if (raw) k_few_z<TB, RT, F32, true, false, FAR><<<grid, block, 0, st>>>(f, e, prep);
+    else k_few_z<TB, RT, F32, false, false, FAR><<<grid, block, 0, st>>>(f, e, prep);
   } else {
-    k_few_z<TB, RT, F32, false, false><<<grid, block, 0, st>>>(f, e, prep);
+    k_few_z<TB, RT, F32, false, false, FAR><<<grid, block, 0, st>>>(f, e, prep);
   }
   return hipGetLastError();
 }
 template <int TB, bool F32>
 hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int rt, int groups, hipStream_t st) {
-  if (rt == 1) return few_z<TB, 1, F32>(f, e, prep, grad, raw, groups, st);
-  return few_z<TB, 4, F32>(f, e, prep, grad, raw, groups, st);
+  if (rt == 1)
+    return f.far ? few_z<TB, 1, F32, true>(f, e, prep, grad, raw, groups, st) : few_z<TB, 1, F32, false>(f, e, prep, grad, raw, groups, st);
+  return f.far ? few_z<TB, 4, F32, true>(f, e, prep, grad, raw, groups, st) : few_z<TB, 4, F32, false>(f, e, prep, grad, raw, groups, st);
 }
 
 template <int TB, bool F32>
 hipError_t few_dx(const XentFew& f, const XentEpi& e, int parts, float* part, hipStream_t st) {
   constexpr int cols = 16 * (F32 ? 4 : 8);
-  k_few_dx<TB, F32><<<dim3((f.k + cols - 1) / cols, parts), dim3(256), 0, st>>>(f, e.dz, e.pitch, e.plane, part);
+  const dim3 grid((f.k + cols - 1) / cols, parts), block(256);
+  if (f.far) k_few_dx<TB, F32, true><<<grid, block, 0, st>>>(f, e.dz, e.pitch, e.plane, part);
+  else k_few_dx<TB, F32, false><<<grid, block, 0, st>>>(f, e.dz, e.pitch, e.plane, part);
   return hipGetLastError();
 }
 

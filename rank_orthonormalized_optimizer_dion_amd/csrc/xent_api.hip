@@ -129,6 +129,7 @@ XentFew few_args(const XentCall& c, const Span& w) {
   f.k = static_cast<int32_t>(c.a.k);
   f.t = static_cast<int32_t>(c.a.t);
   f.tp = c.a.t <= 32 ? 32 : 64;
+  f.far = c.a.n * c.a.k * c.e > kFewFar;
   return f;
 }
 

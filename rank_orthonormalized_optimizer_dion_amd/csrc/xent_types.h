@@ -80,6 +80,11 @@ hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 
 // 100, 64 of them 159).
 constexpr int kXentFewCopied = 64, kXentFew = 32;
 constexpr int kFewDwRows = 64;     // rows of dW of a wavefront
+// Bytes of W from which it is read past the caches, which it would only sweep.
+// Forward and backward in turn, through and past them: 24 tokens in float32, 2048
+// -> 26000 (203 MiB) 237 and 252 us, -> 32000 (250 MiB) 295 and 284; 8 tokens in
+// bfloat16, 4096 -> 32000 (250 MiB) 257 and 223, -> 128000 945 and 914.
+constexpr int64_t kFewFar = int64_t{224} << 20;
 struct XentFew {
   const void* w;           // n rows of k
   int64_t ldw;
@@ -88,6 +93,7 @@ struct XentFew {
   int64_t ldx, xplane;
   int32_t kx;              // columns that are there (and zero from k on)
   int32_t tp;              // tokens of the transposed operands: 32 or 64
+  int32_t far;             // W past the caches
   const uint16_t* xt;      // planes of k x tp
   int64_t xtplane;
   uint16_t* dzt;           // planes of pitch x tp

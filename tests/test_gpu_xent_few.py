@@ -70,6 +70,13 @@ def test_last_row_of_the_weight_not_finite(gpu_lib, dtype):
     assert not bool(dx.any())
 
 
+@pytest.mark.parametrize("t,k,n,dtype", [(3, 4100, 17000, "float32"), (20, 2050, 33000, "float32"), (4, 4097, 33000, "bfloat16"),
+                                         (13, 4104, 33000, "bfloat16"), (50, 4097, 33000, "bfloat16")])
+def test_weights_larger_than_the_caches(gpu_lib, t, k, n, dtype):
+    say(f"cross entropy few, large weight {t} {k} {n} {dtype}")
+    both(gpu_lib, t, k, n, dtype, 0.1)
+
+
 def test_long_vocabulary_in_pieces(gpu_lib):
     """dz of 128 tokens in three planes, by rows and transposed, is bounded by
     pieces of the vocabulary."""
