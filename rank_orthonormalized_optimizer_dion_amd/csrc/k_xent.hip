@@ -62,41 +62,59 @@ __global__ __launch_bounds__(2 * TILE, 2) void k_xent_mm(LinProduct p, XentEpi e
   }
 }
 
-// lse and loss from the partial columns: TOK tokens by 256 / TOK lanes of
-// columns per workgroup.  The loss is formed from differences to the largest
+// lse and loss from the partial columns: TOK tokens by the rest of a workgroup in lanes of
+// columns per workgroup.  1021 tokens of 788 columns: 21 us with 256 threads per
+// 16 tokens, 8 with 1024.  The loss is formed from differences to the largest
 // logit, not from lse, so that a confident prediction's small loss keeps its
 // digits.
 template <int TOK>
-__global__ __launch_bounds__(256) void k_xent_join(XentJoin j) {
-  constexpr int LANES = 256 / TOK;
-  __shared__ float red[3][LANES][TOK];
-  const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK;
-  const int row = blockIdx.x * TOK + tok;
+constexpr int kJoinThreads = TOK == 1 ? 256 : 1024;
+template <int TOK>
+__global__ __launch_bounds__(kJoinThreads<TOK>) void k_xent_join(XentJoin j) {
+  constexpr int LANES = kJoinThreads<TOK> / TOK;
+  static_assert(TOK == 1 || TOK == 16, "the last step has 16 lanes per token");
+  __shared__ float red[3][16][TOK + 1];
+  const int first = blockIdx.x * TOK;
   float top = -INFINITY, sum = 0.0f, total = 0.0f;
-  if (row < j.t) {
+  if (first + static_cast<int>(threadIdx.x) % TOK < j.t) {
+    const int row = first + threadIdx.x % TOK;
 #pragma unroll 4
-    for (int c = lane; c < j.cols; c += LANES) {
+    for (int c = threadIdx.x / TOK; c < j.cols; c += LANES) {
       const int64_t at = static_cast<int64_t>(c) * j.t + row;
       merge(top, sum, j.top[at], j.sum[at]);
       if (j.total) total += j.total[at];
     }
   }
-  red[0][lane][tok] = top;
-  red[1][lane][tok] = sum;
-  red[2][lane][tok] = total;
-  __syncthreads();
+  // to 16 per token, then the 16 lanes of a DPP row
+  const auto of_row = [&] {
+    const float hi = row_max(top);
+    sum = row_sum(sum * exp_fast(top - base_of(hi)));
+    total = row_sum(total);
+    top = hi;
+  };
+  if constexpr (TOK == 1) {
+    of_row();
+  } else {
 #pragma unroll
-  for (int h = LANES / 2; h > 0; h /= 2) {
-    if (lane < h) {
-      merge(top, sum, red[0][lane + h][tok], red[1][lane + h][tok]);
-      total += red[2][lane + h][tok];
-      red[0][lane][tok] = top;
-      red[1][lane][tok] = sum;
-      red[2][lane][tok] = total;
+    for (int h = 16; h < 64; h *= 2) {
+      merge(top, sum, __shfl_xor(top, h), __shfl_xor(sum, h));
+      total += __shfl_xor(total, h);
     }
-    __syncthreads();
   }
-  if (lane != 0 || row >= j.t) return;
+  const int part = TOK == 1 ? threadIdx.x / 16 : threadIdx.x / 64, tok = threadIdx.x % TOK;
+  if (TOK == 1 ? threadIdx.x % 16 == 0 : threadIdx.x % 64 < 16) {
+    red[0][part][tok] = top;
+    red[1][part][tok] = sum;
+    red[2][part][tok] = total;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 16 * TOK) return;
+  top = red[0][threadIdx.x % 16][threadIdx.x / 16];
+  sum = red[1][threadIdx.x % 16][threadIdx.x / 16];
+  total = red[2][threadIdx.x % 16][threadIdx.x / 16];
+  of_row();
+  const int row = first + threadIdx.x / 16;
+  if (threadIdx.x % 16 != 0 || row >= j.t) return;
   const float rest = logf(sum), lse = top + rest;
   if (j.lse) j.lse[row] = lse;
   if (!j.loss) return;
@@ -171,7 +189,7 @@ hipError_t launch_xent_copies(XentCopies a, hipStream_t st) {
 hipError_t launch_xent_join(const XentJoin& j, hipStream_t st) {
   // few tokens: a workgroup each
   if (j.t <= 256) k_xent_join<1><<<dim3(j.t), dim3(256), 0, st>>>(j);
-  else k_xent_join<16><<<dim3((j.t + 15) / 16), dim3(256), 0, st>>>(j);
+  else k_xent_join<16><<<dim3((j.t + 15) / 16), dim3(kJoinThreads<16>), 0, st>>>(j);
   return hipGetLastError();
 }
 
