@@ -75,9 +75,9 @@ struct LinSkinny {
   LinOut out;
 };
 
-// k_lin_skinny up to this many tokens, tiles beyond.  Timed both ways: 17 to 33
-// tokens 2% to 39% faster than tiles (17: 3072 -> 8192 15.2 us against 24.9); 64
-// tokens 768 -> 768 10.5 us against 12.2, but 8192 -> 3072 37.7 us against 29.4.
+// k_lin_skinny up to this many tokens, tiles beyond.  Timed both ways: 17 and 33
+// tokens, 3072 -> 8192 14.7 and 21.3 us against 23.7 and 24.6; 64 tokens 768 -> 768
+// 8.3 us against 9.4, but 8192 -> 3072 37.8 us against 25.9.
 constexpr int kSkinnyTokens = 64;
 // k_lin_rows (float32, or rows not 16-byte aligned) up to this many: 8 tokens
 // of float32 3072 -> 8192 52 us, as split planes on tiles 100 us.

@@ -12,10 +12,9 @@ inline int tile_slots(int tile) { return tile == 256 ? kTileSlots256 : kTileSlot
 
 // Reductions shorter than this are not cut.  Timed over 17 cases of 10 to 100
 // stages: cutting from 10 stages on 8% to 42% slower in eleven (36 matrices of
-// 768 rows 1163 us against 1049; linear, 1000 tokens, 768 -> 768 18.0 us against
-// 12.7), 2% and 11% faster in two (130 x 1000; linear backward, 1000 tokens, 768
-// -> 768 42.6 us against 48.0); from 80 on the same or slower (1000 x 1000
-// float32 528 us against 419).
+// 768 rows 11%; linear, 1000 tokens, 768 -> 768 42%), 2% and 11% faster in two
+// (130 x 1000; linear backward, 1000 tokens, 768 -> 768); from 80 on the same or
+// slower (1000 x 1000 float32 26%).
 constexpr int64_t kMinCutStages = 40;
 
 struct Cut16 {
