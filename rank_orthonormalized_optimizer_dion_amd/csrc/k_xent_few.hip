@@ -124,7 +124,7 @@ __device__ __forceinline__ Planes8<F32 ? 3 : 1> planes16(const Raw16<F32>& r, in
 
 // Pieces of z's reduction that a wavefront loads at a time.
 template <int TB, int RT, bool F32>
-constexpr int kFewZPieces = F32 ? (TB * RT == 1 ? 2 : 1) : TB * RT == 2 ? 4 : TB * RT <= 8 ? 2 : 1;
+constexpr int kFewZPieces = F32 ? (TB * RT == 1 ? 2 : 1) : TB == 2 && RT == 1 ? 4 : TB * RT <= 8 ? 2 : 1;
 
 // Planes of x (zero past its columns) and of its transpose (tokens padded by
 // zeros to a.tp), 64 columns per block.
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(512) void k_few_prep(XentPrep a) {
 // tokens), else from planes whose rows are readable, and zero past k, up to f.kx
 // columns.  With dz, workgroups past the first `prep.first` transpose x for dW.
 template <int TB, int RT, bool F32, bool RAW, bool GRAD, bool FAR>
-__global__ __launch_bounds__(512) void k_few_z(XentFew f, XentEpi e, XentPrep prep) {
+__global__ __launch_bounds__(512, RT == 2 ? 4 : 2) void k_few_z(XentFew f, XentEpi e, XentPrep prep) {
   constexpr int P = F32 ? 3 : 1, ES = F32 ? 4 : 2;
   constexpr int B = (TB + 1) / 2;                       // 512 threads hold 32 tokens by 16 rows of W
   constexpr int RR = RT * TB <= 8 ? RT : 8 / TB;   // blocks of rows that meet in LDS at a time
@@ -342,7 +342,8 @@ __global__ __launch_bounds__(256, 2) void k_few_dx(XentFew f, const uint16_t* dz
   using T = typename std::conditional<F32, float, uint16_t>::type;
   __shared__ float red[2][CW * TB * 4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (blockIdx.x * 16 + (lane & 15)) * CW;
+  // lanes past the last whole group of columns take that one again
+  const int c = min((static_cast<int>(blockIdx.x) * 16 + (lane & 15)) * CW, max(f.k - CW, 0));
   const int steps = (f.n + 31) / 32;
   f32x4 acc[CW][TB];
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(256, 2) void k_few_dx(XentFew f, const uint16_t* dz
   const uint16_t* zr[TB];
 #pragma unroll
   for (int b = 0; b < TB; ++b) zr[b] = dz + min(16 * b + (lane & 15), f.t - 1) * pitch + 8 * (lane >> 4);
-  const bool whole = c + CW <= f.k;
+  const bool whole = CW <= f.k;
 #pragma unroll 2
   for (int s = blockIdx.y * 4 + wave; s < steps; s += 4 * gridDim.y) {
     const int j0 = 32 * s + 8 * (lane >> 4);
@@ -539,6 +540,8 @@ hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool 
 }
 template <int TB, bool F32>
 hipError_t few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool grad, bool raw, int rt, int groups, hipStream_t st) {
+  if constexpr (TB == 1 || (TB == 2 && !F32))
+    if (rt == 2) return few_z<TB, 2, F32, false>(f, e, prep, grad, raw, groups, st);
   if (rt == 1)
     return f.far ? few_z<TB, 1, F32, true>(f, e, prep, grad, raw, groups, st) : few_z<TB, 1, F32, false>(f, e, prep, grad, raw, groups, st);
   return f.far ? few_z<TB, 4, F32, true>(f, e, prep, grad, raw, groups, st) : few_z<TB, 4, F32, false>(f, e, prep, grad, raw, groups, st);
@@ -566,11 +569,24 @@ hipError_t few_dw(const XentFew& f, XentDw d, const XentDxSum& sum, hipStream_t 
 
 }  // namespace
 
-int few_rows(int t, int64_t n) {
-  // 64 rows of W per workgroup where that still makes one per CU: x is read a
-  // quarter as often (24 tokens, 2048 -> 32000: 36 us, 55 with 16 rows; one
-  // token, whose lanes read the same row of x: 34 us, 30 with 16)
-  return t > 4 && n >= 256 * 64 ? 4 : 1;
+int few_rows(int t, int64_t n, bool f32, bool grad, bool far) {
+  // 16 rows of W per workgroup where 64 would not make one per CU, or for a few
+  // tokens, whose lanes read the same rows of x (one token, 2048 -> 32000: 30 us, 34
+  // with 64).
+  if (t <= 4 || n < 256 * 64) return 1;
+  // 64 rows: x is read a quarter as often (24 tokens, 2048 -> 32000: 36 us, 55 with
+  // 16), by one workgroup per CU.  32 rows, by two that fill each other's gaps,
+  // where the registers allow it: dz in bfloat16 up to 32 tokens (24 tokens, 2048
+  // -> 32000: gradients 114 us, 117 with 64; -> 17000 70 and 73; 8 tokens, 768 -> 50257
+  // 68 and 74), but not past the caches (24 tokens, 4096 -> 32000: 220 and 215); the
+  // rest where 64 rows would leave an eighth of the rounds empty (24 tokens, 768 ->
+  // 50257: 26.1 and 29.9; 2048 -> 17000 25.8 and 29.4, but -> 32000 34.7 and 31.4; 8
+  // tokens in float32, 1024 -> 17000 23.3 and 28.4, but 16 tokens, 2048 -> 32000 74 and
+  // 62).
+  const int64_t blocks = (n + 63) / 64, slots = (blocks + 255) / 256 * 256;
+  const bool whole = 8 * blocks >= 7 * slots;
+  if (far || t > (f32 ? 16 : 32)) return 4;
+  return (grad && !f32) || !whole ? 2 : 4;
 }
 
 hipError_t launch_few_prep(const XentPrep& a, bool f32, hipStream_t st) {

@@ -121,6 +121,8 @@ struct XentRun : Run {
   }
 };
 
+bool few_far(const XentCall& c) { return c.a.n * c.a.k * c.e > kFewFar; }
+
 XentFew few_args(const XentCall& c, const Span& w) {
   XentFew f{};
   f.w = w.p;
@@ -129,7 +131,7 @@ XentFew few_args(const XentCall& c, const Span& w) {
   f.k = static_cast<int32_t>(c.a.k);
   f.t = static_cast<int32_t>(c.a.t);
   f.tp = c.a.t <= 32 ? 32 : 64;
-  f.far = c.a.n * c.a.k * c.e > kFewFar;
+  f.far = few_far(c);
   return f;
 }
 
@@ -225,7 +227,7 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const int64_t most_cols = few ? a.n : std::max(kXentStep, (int64_t{1} << 22) / lin_cdiv(a.t, 128) * 128 / kXentStep * kXentStep);
   const int64_t piece = std::min(most_cols, copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n);
   // one partial column per 64 columns at least
-  const int rt = few_rows(static_cast<int>(a.t), a.n);
+  const int rt = few_rows(static_cast<int>(a.t), a.n, c.e == 4, false, few_far(c));
   const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4 * lin_cdiv(a.n, piece);
   XentEpi e{};
   e.target = a.target;
@@ -325,7 +327,7 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
     f.w = wj.p;
     f.n = static_cast<int32_t>(wj.rows);
     e.j0 = static_cast<int32_t>(j0);
-    const int rt = few_rows(f.t, e.pitch);
+    const int rt = few_rows(f.t, e.pitch, f32, true, f.far);
     prep.first = static_cast<int32_t>(few_groups(e.pitch, rt));
     LIN_TRY(launch_few_z(f, e, prep, f32, true, false, rt, 0, r.st));
     prep.xt = nullptr;

@@ -124,7 +124,7 @@ struct XentDxSum {
   int32_t dtype;
 };
 // Blocks of 16 rows of W that a workgroup turns into z at a time.
-int few_rows(int t, int64_t n);
+int few_rows(int t, int64_t n, bool f32, bool grad, bool far);
 // raw: x as it is (at most 16 tokens, no grad); groups: forward's workgroups,
 // each of which leaves one partial column; prep (grad): first, and xt or null
 hipError_t launch_few_z(const XentFew& f, const XentEpi& e, const XentPrep& prep, bool f32, bool grad, bool raw, int rt,

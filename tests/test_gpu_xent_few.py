@@ -70,6 +70,17 @@ def test_last_row_of_the_weight_not_finite(gpu_lib, dtype):
     assert not bool(dx.any())
 
 
+@pytest.mark.parametrize("t", [4, 5, 16, 17, 32])
+@pytest.mark.parametrize("n", [16384, 17001, 32000])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_rows_per_workgroup(gpu_lib, t, n, dtype):
+    """Both sides of the vocabularies and tokens that share W's rows differently,
+    widths that end inside a workgroup's columns."""
+    say(f"cross entropy few, rows {t} {n} {dtype}")
+    both(gpu_lib, t, 200, n, dtype, 0.1)
+    both(gpu_lib, t, 131, n, dtype)
+
+
 @pytest.mark.parametrize("t,k,n,dtype", [(3, 4100, 17000, "float32"), (20, 2050, 33000, "float32"), (4, 4097, 33000, "bfloat16"),
                                          (13, 4104, 33000, "bfloat16"), (50, 4097, 33000, "bfloat16")])
 def test_weights_larger_than_the_caches(gpu_lib, t, k, n, dtype):
