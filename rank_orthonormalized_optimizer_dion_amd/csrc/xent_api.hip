@@ -311,9 +311,12 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
   e.dz = r.ws.take<uint16_t>(planes * e.plane);
   f.dztplane = e.pitch * f.tp;
   f.dzt = r.ws.take<uint16_t>(planes * f.dztplane);
-  // dx: about four workgroups per CU over the columns and the rows of W
+  // dx and dW: as many workgroups as the chip holds at a time, by their registers
+  // (24 tokens, gradients: 768 -> 50257 76 us, with 1024 of either 82; 4096 -> 32000
+  // 198 and 215; 2048 -> 32000 111 and 114)
+  const int64_t dx_slots = f32 ? 1024 : a.t <= 32 ? 768 : 512, dw_slots = 768;
   const int64_t pieces = lin_cdiv(a.n, piece), across = lin_cdiv(a.k, f32 ? 64 : 128);
-  const int64_t parts = std::max<int64_t>(1, std::min(lin_cdiv(1024, across), lin_cdiv(piece, 128)));
+  const int64_t parts = std::max<int64_t>(1, std::min(lin_cdiv(dx_slots, across), lin_cdiv(piece, 128)));
   float* part = a.dx ? r.ws.take<float>(pieces * parts * a.t * a.k) : nullptr;
   if (!r.go) return hipSuccess;
   if (prep.xp) {   // both forms of x before z; else the transpose beside it
@@ -335,9 +338,9 @@ hipError_t xent_backward_few(XentRun& r, const XentCall& c) {
     const bool last = p + 1 == pieces;
     if (a.dw) {
       const Span dj = xent_rows(c.dw, j0, wj.rows);
-      // about four workgroups per CU again, in whole steps of 64 columns
+      // in whole steps of 64 columns
       const int64_t down = lin_cdiv(wj.rows, 4 * kFewDwRows);
-      const int64_t split = std::min(lin_cdiv(a.k, 64), lin_cdiv(1024, down));
+      const int64_t split = std::min(lin_cdiv(a.k, 64), lin_cdiv(dw_slots, down));
       const XentDw d{const_cast<void*>(dj.p), a.lddw, static_cast<int32_t>(lin_cdiv(lin_cdiv(a.k, split), 64) * 64), a.accumulate, 0, 0};
       LIN_TRY(launch_few_dw(f, d, last ? sum : XentDxSum{}, f32, r.st));
     } else if (last) {
