@@ -1,6 +1,6 @@
 // Cross entropy of few tokens (at most 64): reading W once per product, and
 // writing dW, is what it costs, in any type and at any alignment (24 tokens, 2048
-// -> 32000: z 32 us, dx 31, dW 33, each 4.0 to 4.2 TB/s; one token, 768 -> 32000
+// -> 32000: z 36 us, dx 30, dW 31, 3.7 to 4.4 TB/s; one token, 768 -> 32000
 // forward 13.2 us, 11.5 of it k_few_z, 4.3 TB/s).  All products run on the
 // bfloat16 matrix cores with operands that come straight from global memory into
 // registers:

@@ -74,10 +74,10 @@ hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 
 
 // Few tokens (k_xent_few.hip).
 // Tokens: up to 64 in bfloat16 where the tiles would need copies of x or W (2048
-// -> 32000 at an odd pitch, 64 tokens, gradients: 224 us, 65 as tiles 299), up
-// to 32 where they read them in place (32 tokens, gradients: 114 us, 40 as tiles
-// 141; 64 tokens 163 and 143) and in float32 (24 tokens: 78 us forward, 65 as tiles
-// 100, 64 of them 159).
+// -> 32000 at an odd pitch, 64 tokens, forward and gradients: 71 and 212 us, 65 as
+// tiles 110 and 227), up to 32 where they read them in place (32 tokens, gradients:
+// 117 us, 40 as tiles 141; 64 tokens 163 and 143) and in float32 (32 tokens: 82 us
+// forward, 65 as tiles 94, 64 of them 159).
 constexpr int kXentFewCopied = 64, kXentFew = 32;
 constexpr int kFewDwRows = 64;     // rows of dW of a wavefront
 // Bytes of W from which it is read past the caches, which it would only sweep.
