@@ -85,6 +85,15 @@ __device__ __forceinline__ uint32_t dither(uint32_t i, uint32_t seed) {
   return h ^ (h >> 13);
 }
 
+// The root of float32 states' v, within an ulp.  The instruction takes numbers
+// below the normal ones for zero, and a step would then be m / eps, so small v
+// are scaled for it (eps may be far below their roots).
+__device__ __forceinline__ float root_of(float v) {
+  const bool low = v < 0x1p-96f;
+  const float r = __builtin_amdgcn_sqrtf(low ? v * 0x1p32f : v);
+  return low ? r * 0x1p-16f : r;
+}
+
 // Four consecutive elements from i; `left` of them exist.  VEC: as one access
 // where all four exist.  NT: past the caches, which a large step's tensors would
 // only sweep.
@@ -181,8 +190,9 @@ __device__ __forceinline__ void adamw_chunk_of(const AdamwTensor& t, int64_t bas
       g = g * scale;
       m[k] = m[k] * b1 + g * c1;
       v[k] = v[k] * b2 + g * g * c2;
-      r[k] = BITS == 8 ? sqrtf(v[k]) : __builtin_amdgcn_sqrtf(v[k]);
-      // a relative error of 2^-22 in the step is far below X's own rounding
+      r[k] = BITS == 8 ? sqrtf(v[k]) : root_of(v[k]);
+      // a relative error of 2^-22 in the step is far below X's own rounding; the
+      // reciprocal's argument is at least eps, which is a normal number
       x[q][k] = x[q][k] * t.decay - m[k] * rate * __builtin_amdgcn_rcpf(r[k] * root + eps);
     }
     if (left > 0) store4<f32x4, VEC, NT>(t.X, i, left, x[q]);
