@@ -371,7 +371,9 @@ def step_batched(mats: Sequence[Tuple], eta: float, beta: float, variant="orth",
 
 
 class Plan:
-    """A grouped step over a fixed list of matrices (dion_plan_*)."""
+    """A grouped step over a fixed list of matrices (dion_plan_*).  A plan steps
+    the memory that its tensors have when it is made; they must not be given other
+    memory (``X.data = ...``, ``set_``, ``resize_``) while it is used."""
 
     def __init__(self, mats: Sequence[Tuple], variant="orth", math="f32", sharded=False):
         """sharded: the matrices are row shards of global matrices, stepped
@@ -812,15 +814,10 @@ def adamw_state8(X):
     return codes[0], codes[1], scales.view(torch.float8_e8m0fnu)
 
 
-class AdamWPlan:
-    """An AdamW step over a fixed list of tensors: their checks and table once,
-    for many steps."""
+class _AdamWList:
+    """The checks and the table of a list of tensors for AdamW steps."""
 
     def __init__(self, tensors: Sequence[Tuple], weight_decay=0.0):
-        """tensors: (X, G, M, V), M and V float32, or (X, G, M, V, S), M and V
-        float8_e4m3fn and S float8_e8m0fnu (``adamw_state8``); one kind and one
-        type of G for the list.  Contiguous tensors of any shape; X, M, V and S
-        are updated in place.  weight_decay: a number, or one per tensor."""
         torch = _torch()
         count = len(tensors)
         if count == 0:
@@ -859,7 +856,6 @@ class AdamWPlan:
             S = entry[4].data_ptr() if len(entry) == 5 else None
             table[i] = (X.data_ptr(), entry[1].data_ptr(), entry[2].data_ptr(), entry[3].data_ptr(), S, n,
                         float(decay))
-        self._tensors = [tuple(e) for e in tensors]   # keep the tensors alive
         self._table, self.count = table, count
         self._gdtype = 1 if gtype == torch.bfloat16 else 0
         self._run = load().dion_adamw_step_batched
@@ -889,12 +885,34 @@ class AdamWPlan:
             raise _err(rc)
 
 
+class AdamWPlan(_AdamWList):
+    """An AdamW step over a fixed list of tensors: their checks and table once,
+    for many steps.
+
+    A plan steps the memory that its tensors have when it is made, and keeps that
+    memory alive.  So gradients are written into the same G from step to step
+    (``zero_grad(set_to_none=False)``): a new tensor in ``p.grad`` is not seen, the
+    old one's values are used again.  Where a tensor gets other memory (``X.data =
+    ...``, ``set_``, ``resize_``, a module moved), a new plan has to be made; memory
+    that is resized away under a tensor is gone for the plan too."""
+
+    def __init__(self, tensors: Sequence[Tuple], weight_decay=0.0):
+        """tensors: (X, G, M, V), M and V float32, or (X, G, M, V, S), M and V
+        float8_e4m3fn and S float8_e8m0fnu (``adamw_state8``); one kind and one
+        type of G for the list.  Contiguous tensors of any shape; X, M, V and S
+        are updated in place.  weight_decay: a number, or one per tensor."""
+        super().__init__(tensors, weight_decay)
+        # aliases: a tensor may be given other memory, which would free this
+        self._tensors = [tuple(t.detach() for t in e) for e in tensors]
+
+
 def adamw_step_batched(tensors: Sequence[Tuple], lr: float, step: int, betas=(0.9, 0.999),
                        eps: float = 1e-8, weight_decay=0.0, grad_scale=None,
                        seed: Optional[int] = None, stream=None):
     """One AdamW step over a list of (X, G, M, V) or (X, G, M, V, S): see
-    ``AdamWPlan``, which serves many steps over the same tensors."""
-    AdamWPlan(tensors, weight_decay).step(lr, step, betas, eps, grad_scale, seed, stream)
+    ``AdamWPlan``, which serves many steps over the same tensors.  This call keeps
+    nothing and takes gradients wherever they are."""
+    _AdamWList(tensors, weight_decay).step(lr, step, betas, eps, grad_scale, seed, stream)
 
 
 def adamw_step(X, G, M, V, lr: float, step: int, S=None, betas=(0.9, 0.999), eps: float = 1e-8,
