@@ -464,7 +464,7 @@ int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace
  * 0 <= t <= 2^24 (t = 0: dW is zero), 0 <= e <= 1.  Products are taken as the
  * linear layer takes them (bfloat16 exact, float32 as six bfloat16 products),
  * sums in float32; dz is rounded to bfloat16 before its two products (to 16
- * bits with at most 32 tokens, to 24 in float32) and computed a piece of the
+ * bits with at most 64 tokens, to 24 in float32) and computed a piece of the
  * vocabulary at a time, so that the workspace stays near 256 MiB plus, in
  * bfloat16, t x k float32 where there are several pieces and copies of operands
  * that the tiles cannot read in place.  Forward keeps at most an eighth of a

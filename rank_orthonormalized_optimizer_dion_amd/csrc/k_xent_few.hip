@@ -167,7 +167,7 @@ __device__ __forceinline__ void prep_block(const XentPrep& a, int block, float* 
 
 template <bool F32>
 __global__ __launch_bounds__(512) void k_few_prep(XentPrep a) {
-  __shared__ float tile[64 * (kXentFewCopied + 1)];
+  __shared__ float tile[64 * (kXentFew16 + 1)];
   prep_block<F32>(a, blockIdx.x, tile);
 }
 

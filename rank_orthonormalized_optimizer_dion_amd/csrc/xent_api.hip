@@ -83,9 +83,9 @@ int64_t xent_piece(int64_t n, int64_t row) {
 }
 
 // Few tokens: their own kernels (k_xent_few.hip).
-bool xent_few(const XentCall& c) {
-  const bool copied = c.e == 2 && !(lin_direct(c.x) && lin_direct(c.w));
-  return c.a.t <= (copied ? kXentFewCopied : kXentFew);
+bool xent_few(const XentCall& c, bool grad) {
+  const bool copied = !(lin_direct(c.x) && lin_direct(c.w));
+  return c.a.t <= (c.e == 2 && (grad || copied) ? kXentFew16 : kXentFew);
 }
 
 // A call's copies, counters and workspace.
@@ -219,7 +219,7 @@ XentProduct32 xent_product32(XentRun& r, const float* A, int64_t lda, const floa
 hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const dion_cross_entropy& a = c.a;
   if (a.t == 0) return hipSuccess;
-  const bool few = xent_few(c);
+  const bool few = xent_few(c, false);
   const bool f32 = !few && c.e == 4;
   // a piece at a time where W has to be copied, and where one launch would have
   // more threads than a grid can (2^32: 2^22 tiles of 128 x 128, far fewer of others)
@@ -462,7 +462,7 @@ hipError_t xent_backward(XentRun& r, const XentCall& c) {
     LIN_TRY(r.prepare());
     return r.go ? launch_lin_product(dw.p, kLinDw, dw.tile, r.st) : hipSuccess;
   }
-  if (xent_few(c)) return xent_backward_few(r, c);
+  if (xent_few(c, true)) return xent_backward_few(r, c);
   return f32 ? xent_backward_f32(r, c) : xent_backward_bf16(r, c);
 }
 

@@ -73,12 +73,14 @@ enum XentKind32 { kXentStats32 = 0, kXentDz32, kXentDx32, kXentDw32 };
 hipError_t launch_xent_f32(const XentProduct32& p, const XentEpi& e, XentKind32 kind, hipStream_t st);
 
 // Few tokens (k_xent_few.hip).
-// Tokens: up to 64 in bfloat16 where the tiles would need copies of x or W (2048
-// -> 32000 at an odd pitch, 64 tokens, forward and gradients: 71 and 212 us, 65 as
-// tiles 110 and 227), up to 32 where they read them in place (32 tokens, gradients:
-// 117 us, 40 as tiles 141; 64 tokens 163 and 143) and in float32 (32 tokens: 82 us
-// forward, 65 as tiles 94, 64 of them 159).
-constexpr int kXentFewCopied = 64, kXentFew = 32;
+// Tokens: in bfloat16 up to 64 for gradients, whose dz these kernels hold in two
+// planes (as the linear layer's, kLinFewTokens; the tiles hold it in one: 64 tokens,
+// 2048 -> 32000 133 us, as tiles 130; 40 tokens 120 and 129; 64 tokens, 4096 -> 32000
+// 234 and 265, 768 -> 50257 129 and 99), and for the forward where the tiles would
+// need copies of x or W (2048 -> 32000 at an odd pitch, 64 tokens 71 us, 65 as tiles
+// 110); up to 32 in the forward where they read them in place and in float32 (32
+// tokens: 82 us forward, 65 as tiles 94, 64 of them 159).
+constexpr int kXentFew16 = 64, kXentFew = 32;
 constexpr int kFewDwRows = 64;     // rows of dW of a wavefront
 // Bytes of W from which it is read past the caches, which it would only sweep.
 // Forward and backward in turn, through and past them: 24 tokens in float32, 2048
