@@ -465,11 +465,17 @@ int dion_linear_backward(const dion_linear* l, void* workspace, size_t workspace
  * linear layer takes them (bfloat16 exact, float32 as six bfloat16 products),
  * sums in float32; dz is rounded to bfloat16 before its two products (to 16
  * bits with at most 64 tokens, to 24 in float32) and computed a piece of the
- * vocabulary at a time, so that the workspace stays near 256 MiB plus, in
- * bfloat16, t x k float32 where there are several pieces and copies of operands
- * that the tiles cannot read in place.  Forward keeps at most an eighth of a
- * byte per logit (one and a half times that with label smoothing), few tokens up
- * to half a byte, and such copies, of W a piece at a time.
+ * vocabulary at a time.
+ *
+ * The backward's workspace is at most 256 MiB, or 256 columns of dz (2 bytes per
+ * token in bfloat16, 4 in float32) where those are more (from 2^19 and 2^18 tokens
+ * on); 200 MiB of products' partial sums; and in bfloat16 t x k float32 where there
+ * are several pieces, and copies of operands that the tiles cannot read in place,
+ * x and a piece of W (256 MiB, or 256 rows).  With few tokens (64 in bfloat16, 32 in
+ * float32) it is at most 320 MiB and 1 KiB per input.  The forward's is at most an
+ * eighth of a byte per logit (one and a half times that with label smoothing; few
+ * tokens half a byte, of 16384 words at most) and 64 bytes per token, 70 MiB of
+ * partial sums, and such copies.
  *
  * Forward reads x, w, target and writes those of loss and lse that are not
  * NULL.  Backward reads x, w, target, lse (forward's) and dloss and writes

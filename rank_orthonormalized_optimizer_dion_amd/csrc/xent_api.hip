@@ -226,9 +226,9 @@ hipError_t xent_forward(XentRun& r, const XentCall& c) {
   const bool copy = !few && !f32 && !lin_direct(c.w);
   const int64_t most_cols = few ? a.n : std::max(kXentStep, (int64_t{1} << 22) / lin_cdiv(a.t, 128) * 128 / kXentStep * kXentStep);
   const int64_t piece = std::min(most_cols, copy ? xent_piece(a.n, 2 * lin_cdiv(a.k, 64) * 64) : a.n);
-  // one partial column per 64 columns at least
+  // one partial column per 64 columns at least: whole pieces end with a tile
   const int rt = few_rows(static_cast<int>(a.t), a.n, c.e == 4, false, few_far(c));
-  const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4 * lin_cdiv(a.n, piece);
+  const int64_t most = few ? few_groups(a.n, rt) : lin_cdiv(a.n, 64) + 4;
   XentEpi e{};
   e.target = a.target;
   e.ignore = a.ignore_index;
