@@ -1,6 +1,5 @@
 // Device helpers shared by the linear layer and the cross entropy
-// (k_linear.hip, k_xent.hip): element access, plane pairs, and the products of
-// few tokens.
+// (k_linear.hip, k_xent.hip, k_xent_few.hip): element access and plane pairs.
 #pragma once
 #include "linear_types.h"
 #include "mm16.h"
@@ -107,110 +106,6 @@ __device__ __forceinline__ uint16_t first_plane(float x) {
   const uint16_t h = to_bf16(x);
   const uint32_t b = __float_as_uint(x);
   return (h & 0x7fff) == 0x7f80 && (b & 0x7fffffffu) < 0x7f800000u ? static_cast<uint16_t>(b >> 16) : h;
-}
-
-// Few tokens (t <= 16 TB), bfloat16: the weight is read once and that is
-// the cost.  A workgroup owns the 16 rows of W from n0, its 8 wavefronts take
-// turns at 64-element pieces of the reduction (a lane reads 32 consecutive
-// bytes of its row, the two halves feeding two matrix instructions in the same
-// k order for x), and their sums meet in LDS: red[wavefront][token / 16][token
-// % 16][row of W].
-template <int TB>
-__device__ __forceinline__ void skinny_sums(const LinSkinny& p, int n0, float (&red)[8][TB][16][17]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = min(n0 + (lane & 15), p.n - 1);
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + row * p.ldw + 16 * (lane >> 4);
-  const uint16_t* x[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b)
-    x[b] = static_cast<const uint16_t*>(p.x) + min(16 * b + (lane & 15), p.t - 1) * p.ldx + 16 * (lane >> 4);
-  f32x4 acc[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto step = [&](const u32x4 (&a)[2], const u32x4 (&v)[TB][2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[h]),
-                                                         __builtin_bit_cast(bf16x8, v[b][h]), acc[b], 0, 0, 0);
-  };
-  constexpr int U = TB <= 2 ? 4 : 2;   // pieces in flight
-  int k = 64 * wave;
-  for (; k + 64 * 8 * (U - 1) + 64 <= p.k; k += 64 * 8 * U) {
-    u32x4 a[U][2], v[U][TB][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[u][h] = *reinterpret_cast<const u32x4*>(w + k + 512 * u + 8 * h);
-#pragma unroll
-        for (int b = 0; b < TB; ++b) v[u][b][h] = *reinterpret_cast<const u32x4*>(x[b] + k + 512 * u + 8 * h);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) step(a[u], v[u]);
-  }
-  for (; k < p.k; k += 64 * 8) {
-    u32x4 a[2], v[TB][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = k + 16 * (lane >> 4) + 8 * h < p.k;
-      a[h] = in ? *reinterpret_cast<const u32x4*>(w + k + 8 * h) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int b = 0; b < TB; ++b) v[b][h] = in ? *reinterpret_cast<const u32x4*>(x[b] + k + 8 * h) : u32x4{0, 0, 0, 0};
-    }
-    step(a, v);
-  }
-  // 16 x 16 output: lane l, register i holds row 4 (l / 16) + i (of W),
-  // column l % 16 (token)
-#pragma unroll
-  for (int b = 0; b < TB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][b][lane & 15][4 * (lane >> 4) + i] = acc[b][i];
-}
-
-// Few tokens in float32, or bfloat16 rows that are not 16-byte aligned: the
-// products of W's row n with T tokens by one wavefront, float32 multiply-adds
-// over the lanes; every lane has the sums.
-template <int T, bool BF, bool VEC>
-__device__ __forceinline__ void row_sums(const LinSkinny& p, int n, float (&acc)[T]) {
-  constexpr int V = VEC ? (BF ? 8 : 4) : 1;
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < T; ++i) acc[i] = 0.0f;
-  auto get = [&](const void* base, int64_t o, float (&v)[8]) {
-    if constexpr (VEC && BF) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + o);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(u[k] << 16);
-        v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-      }
-    } else if constexpr (VEC) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + o);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = u[k];
-    } else {
-      v[0] = load_value(base, o, BF);
-    }
-  };
-#pragma unroll 4
-  for (int k = V * lane; k < p.k; k += 64 * V) {
-    float a[8], v[8];
-    get(p.w, n * p.ldw + k, a);
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      get(p.x, min(i, p.t - 1) * p.ldx + k, v);
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[i] = fmaf(a[j], v[j], acc[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < T; ++i) {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) acc[i] += __shfl_xor(acc[i], s);
-  }
 }
 
 }  // namespace
