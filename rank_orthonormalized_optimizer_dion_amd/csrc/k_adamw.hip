@@ -76,9 +76,11 @@ __device__ __forceinline__ void values(uint32_t w, float (&x)[4]) {
   x[3] = hi[1];
 }
 
-// The 32 bits of element i's dither: a multiplicative (golden ratio) hash of
-// the index, shifted by the seed, whose upper bits are folded into the lower
-// ones before and after a second multiplication.
+// The 32 bits of element i's dither: the index, shifted by the seed, times a
+// multiplier near 2^32 over the golden ratio, its upper bits folded into the lower
+// ones before and after a second multiplication.  Both multipliers and both
+// shifts are those of the published xxHash32 algorithm (its first two primes and
+// the first two steps of its final mix), whose distribution is known to be good.
 __device__ __forceinline__ uint32_t dither(uint32_t i, uint32_t seed) {
   uint32_t h = (i + seed) * 0x9e3779b1u;
   h = (h ^ (h >> 15)) * 0x85ebca77u;
