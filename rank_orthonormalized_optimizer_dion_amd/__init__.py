@@ -902,8 +902,8 @@ class AdamWPlan(_AdamWList):
         type of G for the list.  Contiguous tensors of any shape; X, M, V and S
         are updated in place.  weight_decay: a number, or one per tensor."""
         super().__init__(tensors, weight_decay)
-        # aliases: a tensor may be given other memory, which would free this
-        self._tensors = [tuple(t.detach() for t in e) for e in tensors]
+        # not the tensors: they may be given other memory, which would free this
+        self._memory = [t.untyped_storage() for e in tensors for t in e]
 
 
 def adamw_step_batched(tensors: Sequence[Tuple], lr: float, step: int, betas=(0.9, 0.999),
